@@ -1,11 +1,12 @@
-"""Builds libcmr.so, the C-ABI library, in-tree with nvcc for sm_100a (B200),
-and libcmr_probe.so, the benchmark's copy-pattern ceiling probe.
+"""Builds the C-ABI libraries in-tree with nvcc for sm_100a (B200): libcmr.so
+(positions and rotation) and libcmr_kv8.so (the paged 8-bit KV cache), and
+libcmr_probe.so, the benchmark's copy-pattern ceiling probe.
 
     python -m vlm_decoder_positional_b200.build [--force] [--verbose-ptxas]
 
 The CUDA runtime is linked statically, so the libraries need only the NVIDIA
 driver at run time.  Only the symbols declared in include/cmr.h are exported
-from libcmr.so.
+from libcmr.so, and those of include/cmr_kv8.h from libcmr_kv8.so.
 """
 import argparse
 import glob
@@ -17,6 +18,8 @@ ROOT = os.path.dirname(PKG)
 INCLUDE = os.path.join(ROOT, "include")
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libcmr.so")
+KV8_DIR = os.path.join(CSRC, "kv8")
+KV8_LIB = os.path.join(PKG, "libcmr_kv8.so")
 PROBE_DIR = os.path.join(PKG, "probe")
 PROBE_LIB = os.path.join(PKG, "libcmr_probe.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
@@ -34,6 +37,10 @@ def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
+def kv8_sources():
+    return sorted(glob.glob(os.path.join(KV8_DIR, "*.cu")))
+
+
 def probe_sources():
     return sorted(glob.glob(os.path.join(PROBE_DIR, "*.cu")))
 
@@ -44,22 +51,26 @@ def _stale(lib, srcs) -> bool:
     t = os.path.getmtime(lib)
     deps = srcs + glob.glob(os.path.join(CSRC, "*.cuh")) + [os.path.join(INCLUDE, "cmr.h"),
                                                            os.path.abspath(__file__)]
+    if lib == KV8_LIB:
+        deps += glob.glob(os.path.join(KV8_DIR, "*.cuh")) + [os.path.join(INCLUDE, "cmr_kv8.h")]
     return any(os.path.getmtime(p) > t for p in deps)
 
 
 def _nvcc(lib, srcs, verbose_ptxas):
     tmp = lib + ".tmp.%d" % os.getpid()
     cmd = [NVCC] + NVCC_FLAGS + (["-Xptxas", "-v"] if verbose_ptxas else []) + [
-        "-I", INCLUDE, "-o", tmp] + srcs
+        "-I", INCLUDE, "-t", "0", "-o", tmp] + srcs
     subprocess.run(cmd, check=True)
     os.replace(tmp, lib)
 
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
-    """Builds libcmr.so (and the probe library) when missing or older than
-    their sources; returns the path of libcmr.so."""
+    """Builds libcmr.so, libcmr_kv8.so and the probe library when missing or
+    older than their sources; returns the path of libcmr.so."""
     if force or _stale(LIB, sources()):
         _nvcc(LIB, sources(), verbose_ptxas)
+    if force or _stale(KV8_LIB, kv8_sources()):
+        _nvcc(KV8_LIB, kv8_sources(), verbose_ptxas)
     if force or _stale(PROBE_LIB, probe_sources()):
         _nvcc(PROBE_LIB, probe_sources(), verbose_ptxas)
     return LIB
