@@ -38,7 +38,8 @@ def sources():
 
 
 def kv8_sources():
-    return sorted(glob.glob(os.path.join(KV8_DIR, "*.cu")))
+    return sorted(glob.glob(os.path.join(KV8_DIR, "*.cu"))) + [
+        os.path.join(CSRC, "tensor_map.cu")]
 
 
 def probe_sources():

@@ -135,6 +135,10 @@ cudaError_t launch_rotate_qk_rows(const RotateArgs& args, const FreqTable& table
 bool encode_bf16_tensor_map(CUtensorMap* map, void* base, int rank, const uint64_t* dims,
                             const uint64_t* strides_bytes, const uint32_t* box,
                             bool swizzle_128b);
+// The same for bytes, with a swizzle of 64 or 128 bytes.
+bool encode_u8_tensor_map(CUtensorMap* map, void* base, int rank, const uint64_t* dims,
+                          const uint64_t* strides_bytes, const uint32_t* box,
+                          int swizzle_bytes);
 // Records, per calling thread, the name of the rotate kernel a launch enqueued
 // (read back through cmr_last_rotate_kernel).
 void note_kernel(const char* name);

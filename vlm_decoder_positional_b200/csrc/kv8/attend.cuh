@@ -1,4 +1,7 @@
-// The two attention kernels' launches and workspaces.
+// What the two attention kernels share: their launches and workspaces, and how
+// a call's query rows are cut into row tiles.  The rows of a KV head are the
+// (token, query head) pairs of its group, token by token; an item is a tile of at
+// most R of them that belong to one sequence.
 #pragma once
 
 #include "kv8.cuh"
@@ -9,6 +12,84 @@ namespace kv8 {
 size_t attend_rows_workspace(int32_t num_seqs, int64_t n_tokens, int32_t hq, int32_t hk,
                              int32_t head_dim);
 cudaError_t launch_attend_rows(const AttendArgs& a, cudaStream_t stream);
+
+// The tcgen05 kernel for many rows (attend_tiles.cu): *launched false, nothing
+// enqueued, when no tensor map can describe the pool.
+size_t attend_tiles_workspace(int32_t num_seqs, int64_t n_tokens, int32_t num_layers, int32_t hq,
+                              int32_t hk, int32_t head_dim);
+cudaError_t launch_attend_tiles(const AttendArgs& a, cudaStream_t stream, bool* launched);
+
+// Item slots per (layer, KV head) that the tokens of a call can need.
+inline int64_t item_slots(int32_t num_seqs, int64_t n_tokens, int group, int R, bool step) {
+  return step ? static_cast<int64_t>(num_seqs) * ((group + R - 1) / R)
+              : n_tokens * group / R + num_seqs;
+}
+
+#ifdef __CUDACC__
+
+struct Item {
+  int32_t b, row;      // sequence and its table row (-1: none)
+  int32_t rows;        // query rows (0: no such item)
+  int32_t first_row;   // index of the first among the sequence's token x group rows
+  int64_t tok;         // first packed token of the sequence
+  int64_t p0;
+  int64_t vis_first;   // tokens that the first and the last row see, within the table
+  int64_t vis_last;
+  bool cut;            // the last row would see beyond the table
+};
+
+// The first slot of sequence b: room enough for the partial tiles before it.
+template <int R>
+__device__ __forceinline__ int64_t item_base(const AttendArgs& a, int64_t b) {
+  return static_cast<int64_t>(__ldg(a.batch.cu + b)) * a.group / R + b;
+}
+
+template <int R>
+__device__ __forceinline__ Item find_item(const AttendArgs& a, int32_t bi, bool* bad) {
+  Item it{};
+  int32_t b, rt;
+  int64_t t0, t1;
+  if (a.batch.cu == nullptr) {
+    const int32_t per = (a.group + R - 1) / R;
+    b = bi / per;
+    rt = bi - b * per;
+    t0 = b;
+    t1 = b + 1;
+  } else {
+    int32_t lo = 0, hi = a.batch.num_seqs;
+    while (hi - lo > 1) {
+      const int32_t mid = (lo + hi) >> 1;
+      if (item_base<R>(a, mid) <= bi)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    b = lo;
+    if (!seq_range(a.batch, b, t0, t1)) {
+      *bad = true;
+      return it;
+    }
+    const int64_t r = bi - item_base<R>(a, b);
+    if (r < 0 || r * R >= (t1 - t0) * a.group) return it;
+    rt = static_cast<int32_t>(r);
+  }
+  const int64_t all = (t1 - t0) * a.group;
+  it.b = b;
+  it.first_row = rt * R;
+  it.rows = static_cast<int32_t>(min(static_cast<int64_t>(R), all - it.first_row));
+  it.tok = t0;
+  it.p0 = a.batch.pos_offset ? __ldg(a.batch.pos_offset + b) : 0;
+  it.row = table_row(a.table, b);
+  const int64_t cap = it.row < 0 ? 0 : static_cast<int64_t>(a.table.max_pages) << a.pool.page_shift;
+  const int64_t f = it.p0 + it.first_row / a.group + 1;
+  const int64_t l = it.p0 + (it.first_row + it.rows - 1) / a.group + 1;
+  it.cut = l > cap;
+  it.vis_first = max(static_cast<int64_t>(0), min(f, cap));
+  it.vis_last = max(static_cast<int64_t>(0), min(l, cap));
+  return it;
+}
+
+#endif  // __CUDACC__
 
 }  // namespace kv8
 }  // namespace cmr

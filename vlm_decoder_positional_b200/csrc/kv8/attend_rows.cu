@@ -75,68 +75,6 @@ struct RowsArgs {
   int32_t* prefix;     // [NB + 1], written by CTA 0 for the joining kernel
 };
 
-// One row tile of one sequence.
-struct Item {
-  int32_t b, row;      // sequence and its table row (-1: none)
-  int32_t rows;        // query rows (0: no such item)
-  int32_t first_row;   // index of the first among the sequence's token x group rows
-  int64_t tok;         // first packed token of the sequence
-  int64_t p0;
-  int64_t vis_first;   // tokens that the first and the last row see, within the table
-  int64_t vis_last;
-  bool cut;            // the last row would see beyond the table
-};
-
-template <int R>
-__device__ __forceinline__ int64_t item_base(const AttendArgs& a, int64_t b) {
-  return static_cast<int64_t>(__ldg(a.batch.cu + b)) * a.group / R + b;
-}
-
-template <int R>
-__device__ Item find_item(const AttendArgs& a, int32_t bi, bool* bad) {
-  Item it{};
-  int32_t b, rt;
-  int64_t t0, t1;
-  if (a.batch.cu == nullptr) {
-    const int32_t per = (a.group + R - 1) / R;
-    b = bi / per;
-    rt = bi - b * per;
-    t0 = b;
-    t1 = b + 1;
-  } else {
-    int32_t lo = 0, hi = a.batch.num_seqs;
-    while (hi - lo > 1) {
-      const int32_t mid = (lo + hi) >> 1;
-      if (item_base<R>(a, mid) <= bi)
-        lo = mid;
-      else
-        hi = mid;
-    }
-    b = lo;
-    if (!seq_range(a.batch, b, t0, t1)) {
-      *bad = true;
-      return it;
-    }
-    const int64_t r = bi - item_base<R>(a, b);
-    if (r < 0 || r * R >= (t1 - t0) * a.group) return it;
-    rt = static_cast<int32_t>(r);
-  }
-  const int64_t all = (t1 - t0) * a.group;
-  it.b = b;
-  it.first_row = rt * R;
-  it.rows = static_cast<int32_t>(min(static_cast<int64_t>(R), all - it.first_row));
-  it.tok = t0;
-  it.p0 = a.batch.pos_offset ? __ldg(a.batch.pos_offset + b) : 0;
-  it.row = table_row(a.table, b);
-  const int64_t cap = it.row < 0 ? 0 : static_cast<int64_t>(a.table.max_pages) << a.pool.page_shift;
-  const int64_t f = it.p0 + it.first_row / a.group + 1;
-  const int64_t l = it.p0 + (it.first_row + it.rows - 1) / a.group + 1;
-  it.cut = l > cap;
-  it.vis_first = max(static_cast<int64_t>(0), min(f, cap));
-  it.vis_last = max(static_cast<int64_t>(0), min(l, cap));
-  return it;
-}
-
 __device__ __forceinline__ int32_t item_tiles(const Item& it) {
   if (it.rows == 0) return 0;
   return max(1, static_cast<int32_t>((it.vis_last + kTile - 1) / kTile));
@@ -815,11 +753,6 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const RowsArg
 // Rows of a tile: 8 where a decode step's group fits them, else 16.
 int rows_of(int group, bool step) { return step && group <= 8 ? 8 : 16; }
 
-int64_t item_slots(int32_t num_seqs, int64_t n_tokens, int group, int R, bool step) {
-  return step ? static_cast<int64_t>(num_seqs) * ((group + R - 1) / R)
-              : n_tokens * group / R + num_seqs;
-}
-
 int max_ctas(int R) {
   const int n = sm_count() * (R == 8 ? 2 : 1);
   return n < kMaxCtas ? n : kMaxCtas;
@@ -896,6 +829,14 @@ cudaError_t launch_attend_rows(const AttendArgs& a, cudaStream_t stream) {
 }
 
 cudaError_t launch_attend(const AttendArgs& a, cudaStream_t stream) {
+  // More than 16 rows per sequence, on average: the tcgen05 kernel, which reads the
+  // cache once for 128 rows.
+  if (a.batch.n_tokens * a.group > 16 * static_cast<int64_t>(a.batch.num_seqs)) {
+    bool launched = false;
+    const cudaError_t e = launch_attend_tiles(a, stream, &launched);
+    if (launched && e == cudaSuccess) note_kernel("attend_tiles_kernel");
+    if (e != cudaSuccess || launched) return e;
+  }
   const cudaError_t e = launch_attend_rows(a, stream);
   if (e == cudaSuccess) note_kernel("attend_rows_kernel");
   return e;
@@ -903,8 +844,9 @@ cudaError_t launch_attend(const AttendArgs& a, cudaStream_t stream) {
 
 size_t attend_workspace_bytes(int32_t num_seqs, int64_t n_tokens, int32_t num_layers, int32_t hq,
                               int32_t hk, int32_t head_dim) {
-  (void)num_layers;
-  return attend_rows_workspace(num_seqs, n_tokens, hq, hk, head_dim);
+  const size_t rows = attend_rows_workspace(num_seqs, n_tokens, hq, hk, head_dim);
+  const size_t tiles = attend_tiles_workspace(num_seqs, n_tokens, num_layers, hq, hk, head_dim);
+  return rows > tiles ? rows : tiles;
 }
 
 }  // namespace kv8

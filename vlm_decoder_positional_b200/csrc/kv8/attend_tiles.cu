@@ -1,0 +1,683 @@
+// Attention over the paged 8-bit cache for calls with many query rows: prompts and
+// chunks, on tcgen05.
+//
+// A CTA takes 128 query rows of a KV head (token x query group) and walks over
+// tiles of 128 cached tokens.  Both products run in kind::f8f6f4 on the codes as
+// they lie in the cache: TMA brings pages into swizzled shared memory, keys are a
+// K-major operand, values an MN-major one, and no code is ever converted.  What
+// is not 8 bits wide is written as a sum of 8-bit numbers:
+//   q = q1 + q2, e4m3, over a power of two per row that brings the row's largest
+//       value into (224, 448]: q1 keeps 4 significant bits, q2 those of the rest,
+//       together bf16's 8 (values below 2^-8 of the largest lose bits under
+//       2^-19 of it);
+//   p = p1 + p2 + p3, e5m2: e5m2 is the upper byte of f16, so with p rounded to 9
+//       significant bits in f16, p1 is its upper byte, p2 that of what is left,
+//       p3 that of the rest, exactly (down to 2^-27 of the row's largest weight).
+// p thus carries the rounding that bf16 weights would (2^-9), and S and O are fp32
+// accumulators in tensor memory.  The scales enter as in attend_rows.cu: keys' in
+// the exponent's factor, values' in the exponent, and 2^-e in the sum of weights.
+//
+// Bound by the tensor cores: 2 x D steps of QK and 3 x 128 of PV at the 8-bit rate
+// (twice bf16's) are 1.25 x the time of the same product in bf16.  Converting V
+// to f16 in shared memory instead (2 x 128 steps' worth) would pay 96 KB of shared
+// memory traffic per tile, more than the third term costs.
+//
+// Warps: 0 loads, 1 issues the products, 4-11 do the softmax: two threads to a
+// row, 64 of a tile's tokens each.  S has two buffers, so QK of the next tile runs
+// while this one's softmax does; p's terms take the place of S.  The reference of
+// the running softmax moves only when weights pass 2^4 times it, and O is scaled
+// again only then.
+#include "attend.cuh"
+#include "kv8.cuh"
+#include "tcgen05.cuh"
+#include "../pdl.cuh"
+#include "../rotate_common.cuh"
+#include "../tma.cuh"
+
+namespace cmr {
+namespace kv8 {
+namespace {
+
+using rot::bf16_hi;
+using rot::bf16_lo;
+using rot::pack_bf16x2;
+
+constexpr int kRows = 128;     // query rows of a CTA
+constexpr int kTile = 128;     // tokens of a tile
+constexpr int kStages = 2;     // K and V tiles in flight
+constexpr int kInfos = 4;      // a tile's scales outlive its keys by the softmax
+constexpr int kSoftmax = 256;  // threads
+constexpr int kFirstWarp = 4;  // of the softmax
+constexpr int kThreads = kSoftmax + 32 * kFirstWarp;
+constexpr int kMaxSplits = 16;
+constexpr float kBase = 11.f;  // weights are at most 2^11 when the reference moves
+constexpr float kLazy = 4.f;   // and 2^15 before it does
+constexpr uint32_t kColumns = 512;
+
+struct TileInfo {
+  float k_scale[8];  // per 16 tokens
+  float v_log2[8];
+  float v_inv[8];
+  uint32_t valid;
+};
+
+template <int D>
+struct Smem {
+  static constexpr int W = D < 128 ? D : 128;  // bytes of a swizzled row
+  static constexpr int kPanel = kTile * W;     // rows x W: also Q's, of 128 rows
+  static constexpr int kTileBytes = kTile * D;
+  static constexpr int kQ = 0;  // two terms
+  static constexpr int kK = 2 * kRows * D;
+  static constexpr int kV = kK + kStages * kTileBytes;
+  static constexpr int kNan = kV + kStages * kTileBytes;
+  static constexpr int kMax = kNan + D * 4;             // [2][2][128] floats
+  static constexpr int kSum = kMax + 4 * kRows * 4;     // [2][128]
+  static constexpr int kInfo = kSum + 2 * kRows * 4;
+  static constexpr int kBars = (kInfo + kInfos * static_cast<int>(sizeof(TileInfo)) + 7) / 8 * 8;
+  static constexpr int kMisc = kBars + 8 * (4 * kStages + 7);
+  static constexpr int kBytes = kMisc + 16 + 1024;  // and room to align
+};
+
+struct TilesArgs {
+  AttendArgs a;
+  int32_t items;   // slots per (layer, head)
+  int32_t splits;  // CTAs of an item
+  float* partial;  // [layers x heads x items][splits][128][D], then the rows' ref and sum
+};
+
+// Byte offset of 16-byte chunk c of row r in a panel.
+template <int W>
+__device__ __forceinline__ int swizzled(int r, int c) {
+  return W == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+}
+
+__device__ __forceinline__ void load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x,
+                                        int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
+  const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// The split of an item's tiles: tiles of one CTA, and how many CTAs have any.
+__device__ __forceinline__ int split_tiles(int nt, int splits) { return (nt + splits - 1) / splits; }
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    attend_tiles_kernel(const TilesArgs ta, const __grid_constant__ CUtensorMap k_map,
+                        const __grid_constant__ CUtensorMap v_map) {
+  using S = Smem<D>;
+  constexpr int W = S::W;
+  constexpr int kPanels = D / W;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024 - (tma::smem_addr(smem_raw) & 1023)) & 1023);
+  const AttendArgs& a = ta.a;
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid & 31;
+  int* s_nan = reinterpret_cast<int*>(smem + S::kNan);
+  float* s_max = reinterpret_cast<float*>(smem + S::kMax);
+  float* s_sum = reinterpret_cast<float*>(smem + S::kSum);
+  TileInfo* s_info = reinterpret_cast<TileInfo*>(smem + S::kInfo);
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + S::kMisc);
+  volatile int* s_dead = reinterpret_cast<volatile int*>(s_tmem + 1);
+  const uint32_t q_smem = tma::smem_addr(smem + S::kQ);
+  const uint32_t k_smem = tma::smem_addr(smem + S::kK);
+  const uint32_t v_smem = tma::smem_addr(smem + S::kV);
+  const uint32_t bars = tma::smem_addr(smem + S::kBars);
+  const uint32_t k_full = bars, k_empty = bars + 8 * kStages;
+  const uint32_t v_full = bars + 16 * kStages, v_empty = bars + 24 * kStages;
+  const uint32_t s_full = bars + 32 * kStages, p_full = s_full + 16;
+  const uint32_t o_done = s_full + 32, q_ready = s_full + 40, drained = s_full + 48;
+
+  // ---- the item: heavy (late) row tiles first
+  const int32_t bi = ta.items - 1 - static_cast<int32_t>(blockIdx.x);
+  const int64_t lh = blockIdx.y;
+  bool bad = false;
+  const Item it = find_item<kRows>(a, bi, &bad);
+  if (tid == 0 && a.status != nullptr && lh == 0 && blockIdx.z == 0) {
+    if (bad) atomicOr(a.status, CMR_DEVICE_BAD_CU_SEQLENS);
+    if (it.rows > 0 && it.cut) atomicOr(a.status, CMR_DEVICE_CACHE_RANGE);
+  }
+  if (it.rows == 0) return;
+  const int vis_first = static_cast<int>(it.vis_first), vis_last = static_cast<int>(it.vis_last);
+  const int all = max(1, (vis_last + kTile - 1) / kTile);
+  const int share = split_tiles(all, ta.splits);
+  const int t0 = blockIdx.z * share;
+  const int nt = min(share, all - t0);
+  if (nt <= 0) return;
+  const bool whole = share == all;
+  const int l = static_cast<int>(lh / a.pool.hk), h = static_cast<int>(lh - l * a.pool.hk);
+
+  if (tid == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      tma::mbar_init(k_full + 8 * s, 1);
+      tma::mbar_init(k_empty + 8 * s, 1);
+      tma::mbar_init(v_full + 8 * s, 1);
+      tma::mbar_init(v_empty + 8 * s, 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      tma::mbar_init(s_full + 8 * s, 2);
+      tma::mbar_init(p_full + 8 * s, kSoftmax / 32);
+    }
+    tma::mbar_init(o_done, 1);
+    tma::mbar_init(drained, 1);
+    tma::mbar_init(q_ready, kSoftmax / 32);
+    tma::mbar_init_fence();
+    *s_dead = 0;
+  }
+  if (warp == 1) tc::alloc(tma::smem_addr(s_tmem), kColumns);
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tmem = *s_tmem;
+  const uint32_t tmem_s[2] = {tmem + 256, tmem + 384};
+
+  // A wait that gives up after its limit ends all later waits of the CTA.
+  auto wait = [&](uint32_t bar, int parity) {
+    if (*s_dead) return;
+    if (!tma::mbar_wait(bar, static_cast<uint32_t>(parity) & 1u)) *s_dead = 1;
+  };
+
+  const int P = 1 << a.pool.page_shift;
+  if (warp == 0) {
+    // ---- loads: lane g < 8 looks after tokens [16g, 16g + 16) of a tile
+    uint32_t problems = 0;
+    auto look = [&](int i, int32_t& unit, float& ks, float& vs) {
+      unit = -1;
+      ks = 0.f;
+      vs = 1.f;
+      const int64_t tok = static_cast<int64_t>(t0 + i) * kTile + 16 * lane;
+      if (lane >= 8 || i >= nt || tok >= vis_last) return;
+      const int32_t id = page_id(a.table, a.pool.num_pages, it.row, tok >> a.pool.page_shift);
+      if (id < 0) {
+        problems |= CMR_DEVICE_CACHE_RANGE;
+        return;
+      }
+      const int64_t u = (static_cast<int64_t>(l) * a.pool.num_pages + id) * a.pool.hk + h;
+      ks = __ldg(a.pool.ks + u);
+      vs = __ldg(a.pool.vs + u);
+      if (scale_ok(ks) && scale_ok(vs)) {
+        unit = static_cast<int32_t>(u);
+      } else {
+        problems |= CMR_DEVICE_BAD_SCALE;
+        vs = 1.f;
+      }
+    };
+    int32_t unit;
+    float ks, vs;
+    look(0, unit, ks, vs);
+    int keys = 0, values = 0;  // tiles whose loads were issued
+    for (int i = 0; i < nt; ++i) {
+      const int stage = i % kStages, parity = (i / kStages - 1) & 1;
+      const uint32_t valid = __ballot_sync(~0u, unit >= 0) & 0xffu;
+      const bool copies = unit >= 0 && (16 * lane) % P == 0;  // first 16 tokens of a page
+      const uint32_t bytes = __popc(__ballot_sync(~0u, copies)) * P * D;
+      // keys
+      if (i >= kStages) wait(k_empty + 8 * stage, parity);
+      __syncwarp();
+      const bool alive = __all_sync(~0u, *s_dead == 0);
+      if (lane < 8) {
+        TileInfo& info = s_info[i % kInfos];
+        info.k_scale[lane] = ks;
+        info.v_log2[lane] = __log2f(vs);
+        info.v_inv[lane] = 1.f / vs;
+        if (lane == 0) info.valid = valid;
+      }
+      __syncwarp();
+      if (!alive) break;
+      if (lane == 0) tma::mbar_arrive_expect_tx(k_full + 8 * stage, bytes);
+      __syncwarp();
+      if (copies)
+        for (int x = 0; x < kPanels; ++x)
+          load_3d(k_smem + stage * S::kTileBytes + x * S::kPanel + 16 * lane * W, &k_map,
+                  k_full + 8 * stage, x * W, 0, unit);
+      ++keys;
+      // values
+      if (i >= kStages) wait(v_empty + 8 * stage, parity);
+      __syncwarp();
+      if (!__all_sync(~0u, *s_dead == 0)) break;
+      if (lane == 0) tma::mbar_arrive_expect_tx(v_full + 8 * stage, bytes);
+      __syncwarp();
+      if (copies)
+        for (int x = 0; x < kPanels; ++x)
+          load_3d(v_smem + stage * S::kTileBytes + x * S::kPanel + 16 * lane * W, &v_map,
+                  v_full + 8 * stage, x * W, 0, unit);
+      ++values;
+      look(i + 1, unit, ks, vs);
+    }
+    // no copy is left in flight when the CTA ends
+    for (int n = max(0, keys - kStages); n < keys; ++n)
+      tma::mbar_wait(k_full + 8 * (n % kStages), (n / kStages) & 1);
+    for (int n = max(0, values - kStages); n < values; ++n)
+      tma::mbar_wait(v_full + 8 * (n % kStages), (n / kStages) & 1);
+    if (problems && a.status != nullptr) atomicOr(a.status, static_cast<int>(problems));
+  } else if (warp == 1) {
+    // ---- products
+    if (lane == 0) {
+      constexpr uint32_t kQkDesc = tc::instruction(tc::kE4M3, tc::kE4M3, false, kTile);
+      constexpr uint32_t kPvDesc = tc::instruction(tc::kE5M2, tc::kE4M3, true, D);
+      wait(q_ready, 0);
+      tc::fence_after();
+      for (int i = 0; i <= nt; ++i) {
+        if (i < nt) {
+          const int stage = i % kStages;
+          wait(k_full + 8 * stage, i / kStages);
+          tc::fence_after();
+          if (!*s_dead) {
+            tma::mbar_arrive(s_full + 8 * (i & 1));  // passes on what the loads wrote beside
+            for (int term = 0; term < 2; ++term)
+              for (int k = 0; k < D / 32; ++k) {
+                const uint32_t at = (k * 32 / W) * S::kPanel + (k * 32) % W;
+                tc::mma_ss(tmem_s[i & 1],
+                           tc::descriptor<W>(q_smem + term * kRows * D + at, 0, 8 * W),
+                           tc::descriptor<W>(k_smem + stage * S::kTileBytes + at, 0, 8 * W),
+                           kQkDesc, term + k > 0);
+              }
+            tc::commit(k_empty + 8 * stage);
+            tc::commit(s_full + 8 * (i & 1));
+          }
+        }
+        if (i > 0) {
+          const int j = i - 1, stage = j % kStages;
+          wait(v_full + 8 * stage, j / kStages);
+          wait(p_full + 8 * (j & 1), j / 2);
+          tc::fence_after();
+          if (!*s_dead) {
+            // groups of 32 tokens that some row sees
+            const int steps = max(1, min(kTile / 32, (vis_last - (t0 + j) * kTile + 31) / 32));
+            for (int term = 0; term < 3; ++term)
+              for (int k = 0; k < steps; ++k)
+                tc::mma_ts(tmem, tmem_s[j & 1] + term * 32 + k * 8,
+                           tc::descriptor<W>(v_smem + stage * S::kTileBytes + k * 32 * W,
+                                             S::kPanel, 8 * W),
+                           kPvDesc, j + term + k > 0);
+            tc::commit(v_empty + 8 * stage);
+            tc::commit(o_done);
+          }
+        }
+      }
+      // nothing of the tensor cores is in flight when tensor memory is freed
+      if (*s_dead) {
+        tc::commit(drained);
+        tma::mbar_wait(drained, 0);
+      }
+    }
+    __syncwarp();
+  } else if (warp >= kFirstWarp) {
+    // ---- softmax: thread (row, half)
+    const int st = tid - 32 * kFirstWarp;
+    const int half = st / kRows, row = st % kRows;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    auto row_at = [&](int r) {
+      const int f = it.first_row + r;
+      const int64_t tok = it.tok + f / a.group;
+      return ((l * a.batch.n_tokens + tok) * a.hq + h * a.group + f % a.group) * D;
+    };
+    for (int d = st; d < D; d += kSoftmax) s_nan[d] = 0x7fffffff;
+
+    // Q over a power of two, as two e4m3 terms
+    float mult;
+    {
+      constexpr int kChunks = D / 2 / 8;  // 16-byte chunks of a half row
+      uint4 x[kChunks];
+      uint32_t mx = 0;
+      const uint4* src = reinterpret_cast<const uint4*>(a.q + row_at(row) + half * (D / 2));
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c) {
+        x[c] = row < it.rows ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+        const uint32_t w[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mx = __vmaxs2(mx, w[i] & 0x7fff7fffu);
+      }
+      mx = max(mx & 0xffffu, mx >> 16);
+      s_max[half * kRows + row] = __uint_as_float(mx);
+      tma::named_sync(1, kSoftmax);
+      mx = max(mx, __float_as_uint(s_max[(1 - half) * kRows + row]));
+      // s = 2^e with max |q| in (224 s, 448 s]
+      int e = static_cast<int>(mx >> 7) - 127 - 8 + ((mx & 0x7fu) > 0x60u ? 1 : 0);
+      e = mx == 0 ? 0 : max(-126, e);
+      const float inv = __int_as_float((127 - e) << 23);
+      mult = mx < 0x7f80u ? a.scale_log2 * __int_as_float((127 + e) << 23)
+                          : __int_as_float(0x7fffffff);  // the row becomes NaN
+#pragma unroll
+      for (int c = 0; c < kChunks; c += 2) {
+        uint32_t t1[4], t2[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint4& y = x[c + i / 2];
+          const uint32_t w0 = i % 2 ? y.z : y.x, w1 = i % 2 ? y.w : y.y;
+          const float q[4] = {bf16_lo(w0) * inv, bf16_hi(w0) * inv, bf16_lo(w1) * inv,
+                              bf16_hi(w1) * inv};
+          const uint32_t a0 = f32_to_e4m3x2(q[0], q[1]), a1 = f32_to_e4m3x2(q[2], q[3]);
+          t1[i] = a0 | (a1 << 16);
+          const uint32_t h0 = e4m3x2_to_f16x2(a0), h1 = e4m3x2_to_f16x2(a1);
+          const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&h0));
+          const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&h1));
+          t2[i] = f32_to_e4m3x2(q[0] - f0.x, q[1] - f0.y) |
+                  (f32_to_e4m3x2(q[2] - f1.x, q[3] - f1.y) << 16);
+        }
+        const int d = half * (D / 2) + 8 * c;  // 16 dims
+        const int off = (d / W) * S::kPanel + swizzled<W>(row, (d % W) / 16);
+        *reinterpret_cast<uint4*>(smem + S::kQ + off) = make_uint4(t1[0], t1[1], t1[2], t1[3]);
+        *reinterpret_cast<uint4*>(smem + S::kQ + kRows * D + off) =
+            make_uint4(t2[0], t2[1], t2[2], t2[3]);
+      }
+      tma::fence_async_shared();
+      __syncwarp();
+      if (lane == 0) tma::mbar_arrive(q_ready);
+    }
+    tma::named_sync(1, kSoftmax);  // the rows' maxima have been read
+    const int seen = row < it.rows
+                         ? static_cast<int>(max(static_cast<int64_t>(0),
+                                                min(it.p0 + (it.first_row + row) / a.group + 1,
+                                                    it.vis_last)))
+                         : 0;
+
+    float ref = -INFINITY, sum = 0.f;
+    for (int i = 0; i < nt; ++i) {
+      const int tile = (t0 + i) * kTile;
+      const TileInfo& info = s_info[i % kInfos];
+      wait(s_full + 8 * (i & 1), i / 2);
+      tc::fence_after();
+      const uint32_t valid = info.valid;
+      const bool edge = tile + kTile > vis_first || valid != 0xffu;
+      uint32_t x[2][32];
+      tc::ld32(x[0], tmem_s[i & 1] + lanes + 64 * half);
+      tc::ld32(x[1], tmem_s[i & 1] + lanes + 64 * half + 32);
+      tc::wait_ld();
+
+      float mx = -INFINITY;
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const float f = mult * info.k_scale[4 * half + g], add = info.v_log2[4 * half + g];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          float y = fmaf(__uint_as_float(x[g / 2][g % 2 * 16 + j]), f, add);
+          if (edge) {
+            const int tok = tile + 64 * half + 16 * g + j;
+            y = tok < seen && ((valid >> (4 * half + g)) & 1u) ? y : -INFINITY;
+          }
+          x[g / 2][g % 2 * 16 + j] = __float_as_uint(y);
+          mx = fmaxf(mx, y);
+        }
+      }
+      // the row's maximum over both halves; every thread has read its part of S
+      float* ex = s_max + (i & 1) * 2 * kRows;
+      ex[half * kRows + row] = mx;
+      tc::fence_before();
+      tma::named_sync(1, kSoftmax);
+      tc::fence_after();
+      mx = fmaxf(mx, ex[(1 - half) * kRows + row]);
+      const bool move = mx > ref + kLazy;
+      if (__any_sync(~0u, move)) {
+        const float to = fmaxf(ref, mx);
+        const float f = to == -INFINITY ? 1.f : exp2_approx(ref - to);
+        ref = to;
+        sum *= f;
+        if (i > 0) {
+          wait(o_done, i - 1);
+          tc::fence_after();
+#pragma unroll
+          for (int c = 0; c < D / 2; c += 32) {
+            uint32_t o[32];
+            tc::ld32(o, tmem + lanes + half * (D / 2) + c);
+            tc::wait_ld();
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+            tc::st32(tmem + lanes + half * (D / 2) + c, o);
+          }
+        }
+      }
+
+      const float shift = (ref == -INFINITY ? 0.f : ref) - kBase;
+      uint32_t t1[16], t2[16], t3[16];
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        float part = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {  // 4 tokens: a word of each term
+          float p[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            p[k] = exp2_approx(__uint_as_float(x[g / 2][g % 2 * 16 + 4 * j + k]) - shift);
+            part += p[k];
+          }
+          // rounded to 9 significant bits, then three times 3 of them
+          const uint32_t a0 = (pack_f16x2(p[0], p[1]) + 0x00020002u) & 0xfffcfffcu;
+          const uint32_t a1 = (pack_f16x2(p[2], p[3]) + 0x00020002u) & 0xfffcfffcu;
+          const uint32_t b0 = sub_f16x2(a0, a0 & 0xff00ff00u), b1 = sub_f16x2(a1, a1 & 0xff00ff00u);
+          const uint32_t c0 = sub_f16x2(b0, b0 & 0xff00ff00u), c1 = sub_f16x2(b1, b1 & 0xff00ff00u);
+          t1[4 * g + j] = __byte_perm(a0, a1, 0x7531);
+          t2[4 * g + j] = __byte_perm(b0, b1, 0x7531);
+          t3[4 * g + j] = __byte_perm(c0, c1, 0x7531);
+        }
+        sum = fmaf(part, info.v_inv[4 * half + g], sum);
+      }
+      tc::st16(tmem_s[i & 1] + lanes + 16 * half, t1);
+      tc::st16(tmem_s[i & 1] + lanes + 32 + 16 * half, t2);
+      tc::st16(tmem_s[i & 1] + lanes + 64 + 16 * half, t3);
+
+      if (edge) {
+        // A weight of zero does not make a NaN vanish: rows that nobody sees are
+        // cleared, and a NaN that some rows see and some do not is taken out and
+        // given back, at the end, to the rows that see it.
+        const int stage = i % kStages;
+        wait(v_full + 8 * stage, i / kStages);
+        uint8_t* v = smem + S::kV + stage * S::kTileBytes;
+        for (int idx = st; idx < S::kTileBytes / 16; idx += kSoftmax) {
+          const int off = idx * 16;
+          const int r = off % S::kPanel / W;
+          const int tok = tile + r;
+          uint4* at = reinterpret_cast<uint4*>(v + off);
+          if (tok >= vis_last || !((valid >> (r / 16)) & 1u)) {
+            *at = make_uint4(0, 0, 0, 0);
+          } else if (tok >= vis_first) {
+            uint4 y = *at;
+            uint32_t w[4] = {y.x, y.y, y.z, y.w};
+            bool any = false;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t nan = ((w[k] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+              if (nan) {
+                any = true;
+                // logical chunk of this place: the swizzle is its own inverse
+                const int c = (swizzled<W>(r, off % W / 16) - r * W) / 16;
+                const int d = off / S::kPanel * W + c * 16 + 4 * k;
+                for (int b = 0; b < 4; ++b)
+                  if (nan & (0x80u << (8 * b))) atomicMin(&s_nan[d + b], tok);
+                w[k] &= ~((nan >> 7) * 0xffu);
+              }
+            }
+            if (any) *at = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+        tma::fence_async_shared();
+      }
+      tc::wait_st();
+      tc::fence_before();
+      __syncwarp();
+      if (lane == 0) tma::mbar_arrive(p_full + 8 * (i & 1));
+    }
+
+    s_sum[half * kRows + row] = sum;
+    tma::named_sync(1, kSoftmax);
+    sum += s_sum[(1 - half) * kRows + row];
+    wait(o_done, nt - 1);
+    tc::fence_after();
+    const float inv = !whole ? 1.f : (sum == 0.f ? 0.f : 1.f / sum);
+    float* rec = ta.partial +
+                 ((lh * ta.items + bi) * ta.splits + blockIdx.z) * (kRows * (D + 2));
+    if (!whole && half == 0) {
+      rec[kRows * D + row] = ref;
+      rec[kRows * D + kRows + row] = sum;
+    }
+#pragma unroll
+    for (int c = 0; c < D / 2; c += 32) {
+      uint32_t o[32];
+      const int d = half * (D / 2) + c;
+      tc::ld32(o, tmem + lanes + d);
+      tc::wait_ld();
+      if (row < it.rows) {
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+          const float y = __uint_as_float(o[k]) * inv;
+          o[k] = __float_as_uint(s_nan[d + k] < seen ? __int_as_float(0x7fffffff) : y);
+        }
+        if (whole) {
+          uint4* dst = reinterpret_cast<uint4*>(a.out + row_at(row) + d);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t w[4];
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+              w[m] = pack_bf16x2(__uint_as_float(o[8 * k + 2 * m]),
+                                 __uint_as_float(o[8 * k + 2 * m + 1]));
+            dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        } else {
+          uint4* dst = reinterpret_cast<uint4*>(rec + row * D + d);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            dst[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+        }
+      }
+    }
+    tc::fence_before();
+  }
+  __syncthreads();
+  if (warp == 1) {
+    tc::fence_after();
+    tc::dealloc(tmem, kColumns);
+  }
+  if (tid == 0 && *s_dead && a.status != nullptr) atomicOr(a.status, CMR_DEVICE_WAIT_TIMEOUT);
+}
+
+constexpr int kJoinThreads = 256;
+
+// Joins the splits of an item: grid (items x layers x heads, row groups).
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) attend_tiles_join_kernel(const TilesArgs ta) {
+  const AttendArgs& a = ta.a;
+  pdl::wait();
+  const int32_t bi = static_cast<int32_t>(blockIdx.x % ta.items);
+  const int64_t lh = blockIdx.x / ta.items;
+  bool bad = false;
+  const Item it = find_item<kRows>(a, bi, &bad);
+  constexpr int kLanes = D / 4;
+  const int r = blockIdx.y * (kJoinThreads / kLanes) + threadIdx.x / kLanes;
+  const int ln = threadIdx.x % kLanes;
+  if (it.rows == 0 || r >= it.rows) return;
+  const int all = max(1, (static_cast<int>(it.vis_last) + kTile - 1) / kTile);
+  const int share = split_tiles(all, ta.splits);
+  if (share == all) return;
+  const int n = (all + share - 1) / share;
+  const float* rec0 = ta.partial + (lh * ta.items + bi) * ta.splits * (kRows * (D + 2));
+  float top = -INFINITY;
+  for (int k = 0; k < n; ++k)
+    top = fmaxf(top, __ldcg(rec0 + k * (kRows * (D + 2)) + kRows * D + r));
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float sum = 0.f;
+#pragma unroll 4
+  for (int k = 0; k < n; ++k) {
+    const float* rec = rec0 + k * (kRows * (D + 2));
+    const float ref = __ldcg(rec + kRows * D + r);
+    const float w = top == -INFINITY ? 0.f : exp2_approx(ref - top);
+    const float4 x = __ldcg(reinterpret_cast<const float4*>(rec + r * D) + ln);
+    sum = fmaf(w, __ldcg(rec + kRows * D + kRows + r), sum);
+    acc.x = fmaf(w, x.x, acc.x);
+    acc.y = fmaf(w, x.y, acc.y);
+    acc.z = fmaf(w, x.z, acc.z);
+    acc.w = fmaf(w, x.w, acc.w);
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  const int l = static_cast<int>(lh / a.pool.hk), h = static_cast<int>(lh - l * a.pool.hk);
+  const int f = it.first_row + r;
+  uint16_t* dst = a.out + ((l * a.batch.n_tokens + it.tok + f / a.group) * a.hq + h * a.group +
+                           f % a.group) * D + 4 * ln;
+  *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv),
+                                              pack_bf16x2(acc.z * inv, acc.w * inv));
+}
+
+// CTAs per item: as many as fill the device once, where the items alone do not
+// fill half of it.
+int splits_for(int64_t items) {
+  const int64_t n = items > 0 ? sm_count() / items : 1;
+  return static_cast<int>(n < 1 ? 1 : (n < kMaxSplits ? n : kMaxSplits));
+}
+
+template <int D>
+cudaError_t launch(const TilesArgs& ta, const CUtensorMap& k, const CUtensorMap& v, int64_t lh,
+                   cudaStream_t stream) {
+  using S = Smem<D>;
+  cudaError_t e = cudaFuncSetAttribute(attend_tiles_kernel<D>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
+  if (e != cudaSuccess) return e;
+  attend_tiles_kernel<D><<<dim3(ta.items, static_cast<unsigned>(lh), ta.splits), kThreads,
+                           S::kBytes, stream>>>(ta, k, v);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || ta.splits == 1) return e;
+  constexpr int kPer = kJoinThreads / (D / 4);
+  return pdl::launch(attend_tiles_join_kernel<D>,
+                     dim3(static_cast<unsigned>(ta.items * lh), kRows / kPer), dim3(kJoinThreads),
+                     0, stream, true, ta);
+}
+
+}  // namespace
+
+size_t attend_tiles_workspace(int32_t num_seqs, int64_t n_tokens, int32_t num_layers, int32_t hq,
+                              int32_t hk, int32_t head_dim) {
+  size_t most = 0;
+  for (const bool step : {false, true}) {
+    const int64_t items = item_slots(num_seqs, n_tokens, hq / hk, kRows, step) * num_layers * hk;
+    const int splits = splits_for(items);
+    if (splits == 1) continue;
+    const size_t bytes = static_cast<size_t>(items) * splits * kRows * (head_dim + 2) * sizeof(float);
+    most = bytes > most ? bytes : most;
+  }
+  return most;
+}
+
+cudaError_t launch_attend_tiles(const AttendArgs& a, cudaStream_t stream, bool* launched) {
+  *launched = false;
+  const Pool& pool = a.pool;
+  const int64_t lh = static_cast<int64_t>(pool.num_layers) * pool.hk;
+  const int64_t units = lh * pool.num_pages;
+  const int64_t items = item_slots(a.batch.num_seqs, a.batch.n_tokens, a.group, kRows,
+                                   a.batch.cu == nullptr);
+  if (lh > 65535 || units > INT32_MAX || items * lh > INT32_MAX) return cudaSuccess;
+  const int D = pool.head_dim;
+  const int W = D < 128 ? D : 128;
+  const uint32_t P = 1u << pool.page_shift;
+  const uint64_t dims[3] = {static_cast<uint64_t>(D), P, static_cast<uint64_t>(units)};
+  const uint64_t strides[2] = {static_cast<uint64_t>(D), static_cast<uint64_t>(D) * P};
+  const uint32_t box[3] = {static_cast<uint32_t>(W), P, 1};
+  CUtensorMap k, v;
+  if (!encode_u8_tensor_map(&k, pool.k, 3, dims, strides, box, W) ||
+      !encode_u8_tensor_map(&v, pool.v, 3, dims, strides, box, W))
+    return cudaSuccess;
+  TilesArgs ta{};
+  ta.a = a;
+  ta.items = static_cast<int32_t>(items);
+  ta.splits = splits_for(items * lh);
+  ta.partial = static_cast<float*>(a.workspace);
+  *launched = true;
+  switch (D) {
+    case 64: return launch<64>(ta, k, v, lh, stream);
+    case 128: return launch<128>(ta, k, v, lh, stream);
+    default: return launch<256>(ta, k, v, lh, stream);
+  }
+}
+
+}  // namespace kv8
+}  // namespace cmr

@@ -29,11 +29,9 @@ EncodeTiledFn encoder() {
   return fn;
 }
 
-}  // namespace
-
-bool encode_bf16_tensor_map(CUtensorMap* map, void* base, int rank, const uint64_t* dims,
-                            const uint64_t* strides_bytes, const uint32_t* box,
-                            bool swizzle_128b) {
+bool encode(CUtensorMap* map, CUtensorMapDataType type, CUtensorMapSwizzle swizzle,
+            CUtensorMapL2promotion promotion, void* base, int rank, const uint64_t* dims,
+            const uint64_t* strides_bytes, const uint32_t* box) {
   const EncodeTiledFn enc = encoder();
   if (enc == nullptr || rank < 1 || rank > 5) return false;
   cuuint64_t d[5], st[4];
@@ -44,10 +42,27 @@ bool encode_bf16_tensor_map(CUtensorMap* map, void* base, int rank, const uint64
     unit[i] = 1;
     if (i + 1 < rank) st[i] = strides_bytes[i];
   }
-  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(rank), base, d, st,
-             b, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             swizzle_128b ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
-             CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return enc(map, type, static_cast<cuuint32_t>(rank), base, d, st, b, unit,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, promotion,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+bool encode_bf16_tensor_map(CUtensorMap* map, void* base, int rank, const uint64_t* dims,
+                            const uint64_t* strides_bytes, const uint32_t* box,
+                            bool swizzle_128b) {
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                swizzle_128b ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                CU_TENSOR_MAP_L2_PROMOTION_NONE, base, rank, dims, strides_bytes, box);
+}
+
+bool encode_u8_tensor_map(CUtensorMap* map, void* base, int rank, const uint64_t* dims,
+                          const uint64_t* strides_bytes, const uint32_t* box,
+                          int swizzle_bytes) {
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8,
+                swizzle_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_128B, base, rank, dims, strides_bytes, box);
 }
 
 int64_t device_l2_bytes() {
