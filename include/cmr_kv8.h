@@ -143,8 +143,9 @@ CMR_API size_t cmr_kv8_attend_workspace_bytes(int32_t num_seqs, int64_t n_tokens
  * the pool in them sets CMR_DEVICE_CACHE_RANGE and is not followed. */
 
 /* Give each named row the pages that it lacks to hold lens[i] tokens (none where
- * it has them).  Entries that find too few free pages left, or that need more
- * than max_pages, get none: CMR_DEVICE_PAGES_FULL or CMR_DEVICE_CACHE_RANGE.
+ * it has them).  An entry that needs more than max_pages gets none
+ * (CMR_DEVICE_CACHE_RANGE); one that finds too few free pages left, and those behind
+ * it that need any, get none (CMR_DEVICE_PAGES_FULL).
  * New pages get page_refs = 1; their codes and scales are left as they are. */
 CMR_API cmr_status cmr_kv8_extend(int32_t* page_table, int32_t table_rows, int32_t max_pages,
                                   int32_t* page_refs, int32_t num_pages, int32_t page_tokens,
@@ -168,12 +169,12 @@ CMR_API cmr_status cmr_kv8_fork(void* k_pages, void* v_pages, float* k_scales, f
                                 int32_t n, void* workspace, size_t workspace_bytes,
                                 int32_t* device_status, cmr_stream_t stream);
 
-/* Empty the named rows: page_refs - 1 for each of their pages (a page at 0 is free),
- * and -1 in every entry of the row. */
+/* Empty the named rows: page_refs - 1 for each of their pages (a page at 0 is free;
+ * one that is at 0 already sets CMR_DEVICE_CACHE_RANGE and stays there), and -1 in
+ * the entries that held them. */
 CMR_API cmr_status cmr_kv8_free(int32_t* page_table, int32_t table_rows, int32_t max_pages,
                                 int32_t* page_refs, int32_t num_pages, const int32_t* slots,
-                                int32_t n, void* workspace, size_t workspace_bytes,
-                                int32_t* device_status, cmr_stream_t stream);
+                                int32_t n, int32_t* device_status, cmr_stream_t stream);
 
 /* Move pages so that those in use are the pool's first: with c pages in use, the
  * ones at c and above go, in order, to the free ones below c, in every layer,
@@ -186,7 +187,7 @@ CMR_API cmr_status cmr_kv8_compact(void* k_pages, void* v_pages, float* k_scales
                                    int32_t* page_refs, void* workspace, size_t workspace_bytes,
                                    int32_t* device_status, cmr_stream_t stream);
 
-/* Workspace bytes of the four calls above (n = 0 for cmr_kv8_compact).  No CUDA
+/* Workspace bytes of the calls above that take one (n = 0 for cmr_kv8_compact).  No CUDA
  * call is made. */
 CMR_API size_t cmr_kv8_pages_workspace_bytes(int32_t table_rows, int32_t num_pages, int32_t n);
 

@@ -178,26 +178,29 @@ cmr_status check_rotation(double theta, const int32_t sections[3], int32_t rot_d
   return CMR_OK;
 }
 
-// Shared by the page calls: table, counts, list of rows, workspace.
+// Shared by the page calls: table, counts, list of rows.
 cmr_status check_pages(int32_t* page_table, int32_t table_rows, int32_t max_pages,
-                       int32_t* page_refs, int32_t num_pages, int32_t n, void* workspace,
-                       size_t workspace_bytes, cmr::kv8::PagesArgs* a) {
+                       int32_t* page_refs, int32_t num_pages, int32_t n,
+                       cmr::kv8::PagesArgs* a) {
   if (n < 0) return fail(CMR_EINVAL, "negative n");
   if (num_pages < 1) return fail(CMR_EINVAL, "num_pages must be >= 1");
   cmr_status s;
   if ((s = check_table(page_table, table_rows, max_pages)) != CMR_OK) return s;
   if ((s = check(page_refs, "page_refs")) != CMR_OK) return s;
-  if ((s = check_workspace(workspace, workspace_bytes,
-                           cmr::kv8::pages_workspace_bytes(table_rows, num_pages, n))) != CMR_OK)
-    return s;
   a->pool.num_pages = num_pages;
   a->table = page_table;
   a->rows = table_rows;
   a->max_pages = max_pages;
   a->refs = page_refs;
   a->n = n;
-  a->workspace = static_cast<int32_t*>(workspace);
   return CMR_OK;
+}
+
+cmr_status check_pages_workspace(void* workspace, size_t workspace_bytes,
+                                 cmr::kv8::PagesArgs* a) {
+  a->workspace = static_cast<int32_t*>(workspace);
+  return check_workspace(workspace, workspace_bytes,
+                         cmr::kv8::pages_workspace_bytes(a->rows, a->pool.num_pages, a->n));
 }
 
 }  // namespace
@@ -361,9 +364,9 @@ cmr_status cmr_kv8_extend(int32_t* page_table, int32_t table_rows, int32_t max_p
   cmr_status s;
   if (page_shift(page_tokens) < 0)
     return fail(CMR_EUNSUPPORTED, "page_tokens must be 16, 32, 64 or 128, got %d", page_tokens);
-  if ((s = check_pages(page_table, table_rows, max_pages, page_refs, num_pages, n, workspace,
-                       workspace_bytes, &a)) != CMR_OK)
+  if ((s = check_pages(page_table, table_rows, max_pages, page_refs, num_pages, n, &a)) != CMR_OK)
     return s;
+  if ((s = check_pages_workspace(workspace, workspace_bytes, &a)) != CMR_OK) return s;
   if (n == 0) return CMR_OK;
   if ((s = check(slots, "slots")) != CMR_OK) return s;
   if ((s = check(lens, "lens")) != CMR_OK) return s;
@@ -387,9 +390,9 @@ cmr_status cmr_kv8_fork(void* k_pages, void* v_pages, float* k_scales, float* v_
                         size_t workspace_bytes, int32_t* device_status, cmr_stream_t stream) {
   cmr::kv8::PagesArgs a{};
   cmr_status s;
-  if ((s = check_pages(page_table, table_rows, max_pages, page_refs, num_pages, n, workspace,
-                       workspace_bytes, &a)) != CMR_OK)
+  if ((s = check_pages(page_table, table_rows, max_pages, page_refs, num_pages, n, &a)) != CMR_OK)
     return s;
+  if ((s = check_pages_workspace(workspace, workspace_bytes, &a)) != CMR_OK) return s;
   if ((s = check_pool(k_pages, v_pages, k_scales, v_scales, num_layers, hk, head_dim, num_pages,
                       page_tokens, &a.pool)) != CMR_OK)
     return s;
@@ -413,17 +416,15 @@ cmr_status cmr_kv8_fork(void* k_pages, void* v_pages, float* k_scales, float* v_
 
 cmr_status cmr_kv8_free(int32_t* page_table, int32_t table_rows, int32_t max_pages,
                         int32_t* page_refs, int32_t num_pages, const int32_t* slots, int32_t n,
-                        void* workspace, size_t workspace_bytes, int32_t* device_status,
-                        cmr_stream_t stream) {
+                        int32_t* device_status, cmr_stream_t stream) {
   cmr::kv8::PagesArgs a{};
   cmr_status s;
-  if ((s = check_pages(page_table, table_rows, max_pages, page_refs, num_pages, n, workspace,
-                       workspace_bytes, &a)) != CMR_OK)
+  if ((s = check_pages(page_table, table_rows, max_pages, page_refs, num_pages, n, &a)) != CMR_OK)
     return s;
   if (n == 0) return CMR_OK;
   if ((s = check(slots, "slots")) != CMR_OK) return s;
   const Named list[] = {{page_table, "page_table"}, {page_refs, "page_refs"}, {slots, "slots"},
-                        {workspace, "workspace"}, {device_status, "device_status"}};
+                        {device_status, "device_status"}};
   if ((s = all_on_device(list)) != CMR_OK) return s;
   a.dst = slots;
   a.status = device_status;
@@ -438,9 +439,9 @@ cmr_status cmr_kv8_compact(void* k_pages, void* v_pages, float* k_scales, float*
                            size_t workspace_bytes, int32_t* device_status, cmr_stream_t stream) {
   cmr::kv8::PagesArgs a{};
   cmr_status s;
-  if ((s = check_pages(page_table, table_rows, max_pages, page_refs, num_pages, 0, workspace,
-                       workspace_bytes, &a)) != CMR_OK)
+  if ((s = check_pages(page_table, table_rows, max_pages, page_refs, num_pages, 0, &a)) != CMR_OK)
     return s;
+  if ((s = check_pages_workspace(workspace, workspace_bytes, &a)) != CMR_OK) return s;
   if ((s = check_pool(k_pages, v_pages, k_scales, v_scales, num_layers, hk, head_dim, num_pages,
                       page_tokens, &a.pool)) != CMR_OK)
     return s;

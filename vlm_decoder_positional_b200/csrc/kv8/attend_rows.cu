@@ -59,12 +59,12 @@ struct Smem {
   static constexpr int kStages = NQ == 1 ? 3 : 2;
   static constexpr int kStage = 2 * kTile * D;
   static constexpr int kQ = kStages * kStage;                      // f16 fragments of Q
-  static constexpr int kO = kQ + (D / 16) * NQ * 32 * 8;           // [R][D + 4] floats
-  static constexpr int kNan = kO + R * (D + 4) * 4;                // [D] ints
-  static constexpr int kRow = kNan + D * 4;                        // per row: see below
-  static constexpr int kInfo = kRow + 4 * (2 * R + 2 * kWarps * R);
+  static constexpr int kNan = kQ + (D / 16) * NQ * 32 * 8;         // [2][D] ints
+  static constexpr int kRow = kNan + 2 * D * 4;                    // [2] of the rows' words
+  static constexpr int kRowWords = 2 * R + 2 * kWarps * R;
+  static constexpr int kInfo = kRow + 2 * 4 * kRowWords;
   static constexpr int kBars = (kInfo + kStages * static_cast<int>(sizeof(StageInfo)) + 7) / 8 * 8;
-  static constexpr int kPrefix = (kBars + 16 * kStages + 15) / 16 * 16;  // [items + 1] ints
+  static constexpr int kItems = (kBars + 16 * kStages + 15) / 16 * 16;  // 3 ints an item, and 1
 };
 
 struct RowsArgs {
@@ -73,6 +73,8 @@ struct RowsArgs {
   int32_t ctas;        // CTAs of the split form; 0: one CTA per item
   float* partial;      // [ctas][2][R][D + 2]
   int32_t* prefix;     // [NB + 1], written by CTA 0 for the joining kernel
+  int4* left;          // [ctas]: the item that a run starts and leaves to others to end
+                       // (layer x head, item, last CTA, place of the first piece), or -1
 };
 
 __device__ __forceinline__ int32_t item_tiles(const Item& it) {
@@ -110,201 +112,186 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
       : "memory");
 }
 
-// The run of tiles [lo, hi) of this CTA, and the walk over the items in it.
-struct Run {
-  int64_t lo, hi;
-  int32_t total;  // tiles per (layer, head)
-};
+// Work is counted in tiles, and kLead more for each item: what it costs to start
+// and to finish one.  Places [start, start + kLead) of an item's stretch hold no
+// tile.
+constexpr int kLead = 2;
 
 template <int D, int NQ>
 __global__ void __launch_bounds__(kThreads, NQ == 1 ? 2 : 1) attend_rows_kernel(const RowsArgs ra) {
   using S = Smem<D, NQ>;
   constexpr int R = S::R;
   constexpr int NS = S::kStages;
+  constexpr int M = D / 16;  // O^T's row blocks
   extern __shared__ __align__(128) uint8_t smem[];
   const AttendArgs& a = ra.a;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid & 31;
   uint2* s_q = reinterpret_cast<uint2*>(smem + S::kQ);
-  float* s_o = reinterpret_cast<float*>(smem + S::kO);
-  int* s_nan = reinterpret_cast<int*>(smem + S::kNan);
-  float* s_mult = reinterpret_cast<float*>(smem + S::kRow);        // [R] score to log2 weight
-  int* s_vis = reinterpret_cast<int*>(s_mult + R);                 // [R] tokens seen
-  float* s_ref = reinterpret_cast<float*>(s_vis + R);              // [warps][R]
-  float* s_sum = s_ref + kWarps * R;                               // [warps][R]
   StageInfo* s_info = reinterpret_cast<StageInfo*>(smem + S::kInfo);
-  int* s_prefix = reinterpret_cast<int*>(smem + S::kPrefix);
+  const int NB = ra.items;
+  const int kept = ra.ctas > 0 ? NB : 1;                              // items of this CTA's list
+  int* s_prefix = reinterpret_cast<int*>(smem + S::kItems);           // [kept + 1]
+  int* s_seen = s_prefix + kept + 1;                                  // [kept] vis_last
+  int* s_row = s_seen + kept;                                         // [kept] table row
   const uint32_t stage0 = tma::smem_addr(smem);
   const uint32_t full0 = tma::smem_addr(smem + S::kBars);
   const uint32_t empty0 = full0 + 8 * NS;
 
   if (tid == 0) {
     for (int s = 0; s < NS; ++s) {
-      tma::mbar_init(full0 + 8 * s, 1);
+      tma::mbar_init(full0 + 8 * s, 2);
       tma::mbar_init(empty0 + 8 * s, kWarps);
     }
     tma::mbar_init_fence();
   }
+  // ---- the items and this CTA's run [lo, hi) of the work
   bool bad = false;
-  const int NB = ra.items;
-  Run run;
-  int32_t only = -1;  // the item of a CTA that has one
-  int64_t item0 = 0;  // (layer, head) of it
-  if (ra.ctas > 0) {
-    for (int i = tid; i < NB; i += kThreads) {
-      const Item it = find_item<R>(a, i, &bad);
-      s_prefix[i] = item_tiles(it);
-      if (blockIdx.x == 0 && it.rows > 0 && it.cut && a.status != nullptr)
-        atomicOr(a.status, CMR_DEVICE_CACHE_RANGE);
-    }
-    if (bad && blockIdx.x == 0 && a.status != nullptr)
-      atomicOr(a.status, CMR_DEVICE_BAD_CU_SEQLENS);
-    __syncthreads();
-    if (warp == 0) {  // exclusive scan in place
-      int carry = 0;
-      for (int i0 = 0; i0 < NB; i0 += 32) {
-        const int i = i0 + lane;
-        const int v = i < NB ? s_prefix[i] : 0;
-        int x = v;
+  const int first = ra.ctas > 0 ? 0 : blockIdx.x;  // item number of list entry 0
+  for (int i = tid; i < kept; i += kThreads) {
+    const Item it = find_item<R>(a, first + i, &bad);
+    const int tiles = item_tiles(it);
+    s_prefix[i] = tiles > 0 ? tiles + kLead : 0;
+    s_seen[i] = static_cast<int>(it.vis_last);
+    s_row[i] = it.row;
+    if ((ra.ctas > 0 ? blockIdx.x == 0 : blockIdx.y == 0) && it.rows > 0 && it.cut &&
+        a.status != nullptr)
+      atomicOr(a.status, CMR_DEVICE_CACHE_RANGE);
+  }
+  if (bad && (ra.ctas > 0 ? blockIdx.x == 0 : blockIdx.y == 0) && a.status != nullptr)
+    atomicOr(a.status, CMR_DEVICE_BAD_CU_SEQLENS);
+  __syncthreads();
+  if (warp == 0) {  // exclusive scan in place
+    int carry = 0;
+    for (int i0 = 0; i0 < kept; i0 += 32) {
+      const int i = i0 + lane;
+      const int v = i < kept ? s_prefix[i] : 0;
+      int x = v;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int y = __shfl_up_sync(~0u, x, o);
-          if (lane >= o) x += y;
-        }
-        if (i < NB) s_prefix[i] = carry + x - v;
-        carry += __shfl_sync(~0u, x, 31);
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(~0u, x, o);
+        if (lane >= o) x += y;
       }
-      if (lane == 0) s_prefix[NB] = carry;
+      __syncwarp();
+      if (i < kept) s_prefix[i] = carry + x - v;
+      carry += __shfl_sync(~0u, x, 31);
     }
-    __syncthreads();
+    if (lane == 0) s_prefix[kept] = carry;
+  }
+  __syncthreads();
+  const int32_t total = s_prefix[kept];  // per (layer, head)
+  int64_t run_lo, run_hi, lh0 = 0;
+  if (ra.ctas > 0) {
     if (blockIdx.x == 0)
       for (int i = tid; i <= NB; i += kThreads) ra.prefix[i] = s_prefix[i];
-    run.total = s_prefix[NB];
-    const int64_t all = static_cast<int64_t>(run.total) * a.pool.num_layers * a.pool.hk;
+    const int64_t all = static_cast<int64_t>(total) * a.pool.num_layers * a.pool.hk;
     const int64_t per = (all + ra.ctas - 1) / ra.ctas;
-    run.lo = min(all, blockIdx.x * per);
-    run.hi = min(all, run.lo + per);
+    run_lo = min(all, blockIdx.x * per);
+    run_hi = min(all, run_lo + per);
   } else {
-    only = blockIdx.x;
-    item0 = blockIdx.y;
-    const Item it = find_item<R>(a, only, &bad);
-    if (tid == 0 && a.status != nullptr && item0 == 0) {
-      if (bad) atomicOr(a.status, CMR_DEVICE_BAD_CU_SEQLENS);
-      if (it.rows > 0 && it.cut) atomicOr(a.status, CMR_DEVICE_CACHE_RANGE);
-    }
-    run.total = item_tiles(it);
-    run.lo = 0;
-    run.hi = run.total;
-    __syncthreads();
+    lh0 = blockIdx.y;
+    run_lo = 0;
+    run_hi = total;
   }
   pdl::launch_dependents();
 
-  // The segment of the run that starts at tile w: its (layer, head), item, first
-  // tile and tile count, and whether it is the whole item.
-  auto segment = [&](int64_t w, int64_t& lh, int32_t& bi, int32_t& t0, int32_t& nt, bool& whole) {
-    if (only >= 0) {
-      lh = item0;
-      bi = only;
-      t0 = 0;
-      nt = run.total;
-      whole = true;
-      return;
-    }
-    lh = w / run.total;
-    const int32_t r = static_cast<int32_t>(w - lh * run.total);
-    int32_t lo = 0, hi = NB;
-    while (hi - lo > 1) {  // the last item that starts at or before r
+  // Entry of the list at place r of a (layer, head)'s work.
+  auto entry_at = [&](int32_t r) {
+    int32_t lo = 0, hi = kept;
+    while (hi - lo > 1) {  // the last that starts at or before r
       const int32_t mid = (lo + hi) >> 1;
       if (s_prefix[mid] <= r)
         lo = mid;
       else
         hi = mid;
     }
-    bi = lo;
-    t0 = r - s_prefix[lo];
-    const int32_t left = s_prefix[lo + 1] - r;
-    nt = static_cast<int32_t>(min(static_cast<int64_t>(left), run.hi - w));
-    whole = t0 == 0 && nt == left;
+    return lo;
   };
 
   const int P = 1 << a.pool.page_shift;
   if (warp == kWarps) {
-    // ---- producer: lane 4 i + g looks after tokens [16g, 16g + 16) of tile i of
-    // a batch of eight tiles
+    // ---- producer: lane 4 i + g looks after tokens [16g, 16g + 16) of place i of a
+    // batch of eight
+    const int g = lane & 3;
+    const int span = min(P, kTile);
+    uint32_t problems = 0;
+    struct Look {
+      bool tile;      // the place holds a tile
+      int64_t unit;   // its page's (layer, page, head), or -1
+      int rows;       // rows that this lane copies
+      int64_t tok;
+      float ks, vs;
+    };
+    auto look = [&](int64_t w0) {
+      Look k{false, -1, 0, 0, 0.f, 1.f};
+      const int64_t w = w0 + (lane >> 2);
+      if (w >= run_hi) return k;
+      const int64_t lh = w / max(total, 1);
+      const int32_t r = static_cast<int32_t>(w - lh * total);
+      const int32_t e = entry_at(r);
+      const int32_t tile = r - s_prefix[e] - kLead;
+      if (tile < 0) return k;
+      k.tile = true;
+      k.tok = static_cast<int64_t>(tile) * kTile + 16 * g;
+      const int seen = s_seen[e];
+      if (k.tok >= seen) return k;
+      const int32_t id = page_id(a.table, a.pool.num_pages, s_row[e], k.tok >> a.pool.page_shift);
+      if (id < 0) {
+        problems |= CMR_DEVICE_CACHE_RANGE;
+        return k;
+      }
+      const int l = static_cast<int>((lh + lh0) / a.pool.hk);
+      const int h = static_cast<int>((lh + lh0) - static_cast<int64_t>(l) * a.pool.hk);
+      k.unit = (static_cast<int64_t>(l) * a.pool.num_pages + id) * a.pool.hk + h;
+      k.ks = __ldg(a.pool.ks + k.unit);
+      k.vs = __ldg(a.pool.vs + k.unit);
+      // the lane that copies for a page (or for 64 tokens of a larger one) takes
+      // the rows up to the last one seen, in whole groups of 16
+      if ((16 * g) % span == 0)
+        k.rows = static_cast<int>(min(static_cast<int64_t>(span), (seen - k.tok + 15) / 16 * 16));
+      return k;
+    };
     int stage = 0, phase = 0, issued = 0;
     bool dead = false;
-    uint32_t problems = 0;
-    for (int64_t w = run.lo; w < run.hi && !dead;) {
-      int64_t lh;
-      int32_t bi, t0, nt;
-      bool whole;
-      segment(w, lh, bi, t0, nt, whole);
-      w += nt;
-      bool ignored = false;
-      const Item it = find_item<R>(a, bi, &ignored);
-      const int l = static_cast<int>(lh / a.pool.hk), h = static_cast<int>(lh - l * a.pool.hk);
-      const int g = lane & 3;
-      for (int tb = 0; tb < nt && !dead; tb += 8) {
-        const int tile = tb + (lane >> 2);
-        const int64_t tok = static_cast<int64_t>(t0 + tile) * kTile + 16 * g;
-        int32_t id = -1;
-        float ks = 0.f, vs = 1.f;
-        int64_t unit = 0;
-        const bool wanted = tile < nt && tok < it.vis_last;
-        if (wanted) {
-          id = page_id(a.table, a.pool.num_pages, it.row, tok >> a.pool.page_shift);
-          if (id >= 0) {
-            unit = (static_cast<int64_t>(l) * a.pool.num_pages + id) * a.pool.hk + h;
-            ks = __ldg(a.pool.ks + unit);
-            vs = __ldg(a.pool.vs + unit);
-            if (!scale_ok(ks) || !scale_ok(vs)) {
-              problems |= CMR_DEVICE_BAD_SCALE;
-              id = -1;
-              vs = 1.f;
-            }
-          } else {
-            problems |= CMR_DEVICE_CACHE_RANGE;
-          }
+    Look now = look(run_lo);
+    for (int64_t w = run_lo; w < run_hi && !dead; w += 8) {
+      const uint32_t tiles = __ballot_sync(~0u, now.tile);
+      int bytes = now.rows + __shfl_xor_sync(~0u, now.rows, 1);
+      bytes = (bytes + __shfl_xor_sync(~0u, bytes, 2)) * 2 * D;
+      for (int i = 0; i < 8; ++i) {
+        if (!((tiles >> (4 * i)) & 1u)) continue;
+        if (issued >= NS && !tma::mbar_wait(empty0 + 8 * stage, phase ^ 1)) dead = true;
+        dead = __any_sync(~0u, dead);
+        if (dead) break;
+        const uint32_t bar = full0 + 8 * stage;
+        if (lane == 4 * i) tma::mbar_arrive_expect_tx(bar, bytes);
+        __syncwarp();
+        const bool mine = (lane >> 2) == i;
+        if (mine && now.rows > 0) {
+          const int64_t src = now.unit * (static_cast<int64_t>(P) * D) + (now.tok & (P - 1)) * D;
+          const uint32_t dst = stage0 + stage * S::kStage + 16 * g * D;
+          bulk_load(dst, a.pool.k + src, now.rows * D, bar);
+          bulk_load(dst + kTile * D, a.pool.v + src, now.rows * D, bar);
         }
-        const uint32_t valid = __ballot_sync(~0u, id >= 0);
-        // the lane that copies for a page (or for 64 tokens of a larger one) takes
-        // the rows up to the last one seen, in whole groups of 16
-        const int span = min(P, kTile);
-        int rows = 0;
-        if (id >= 0 && (16 * g) % span == 0) {
-          const int64_t left = it.vis_last - tok;
-          rows = static_cast<int>(min(static_cast<int64_t>(span), (left + 15) / 16 * 16));
+        // the scales, under the copies
+        const bool good = now.unit >= 0 && scale_ok(now.ks) && scale_ok(now.vs);
+        if (mine && now.unit >= 0 && !good) problems |= CMR_DEVICE_BAD_SCALE;
+        const uint32_t valid = __ballot_sync(~0u, good);
+        if (mine) {
+          StageInfo& info = s_info[stage];
+          info.k_scale[g] = good ? now.ks : 0.f;
+          info.v_log2[g] = good ? __log2f(now.vs) : 0.f;
+          info.v_inv[g] = good ? 1.f / now.vs : 1.f;
+          if (g == 0) info.valid = (valid >> (4 * i)) & 15u;
         }
-        int quad_rows = rows + __shfl_xor_sync(~0u, rows, 1);
-        quad_rows += __shfl_xor_sync(~0u, quad_rows, 2);
-        const int tiles = min(8, nt - tb);
-        for (int i = 0; i < tiles; ++i) {
-          if (issued >= NS && !tma::mbar_wait(empty0 + 8 * stage, phase ^ 1)) dead = true;
-          dead = __any_sync(~0u, dead);
-          if (dead) break;
-          if ((lane >> 2) == i) {
-            StageInfo& info = s_info[stage];
-            info.k_scale[g] = ks;
-            info.v_log2[g] = __log2f(vs);
-            info.v_inv[g] = 1.f / vs;
-            if (g == 0) info.valid = (valid >> (4 * i)) & 15u;
-          }
-          __syncwarp();
-          const uint32_t bar = full0 + 8 * stage;
-          if (lane == 4 * i) tma::mbar_arrive_expect_tx(bar, 2u * quad_rows * D);
-          __syncwarp();
-          if ((lane >> 2) == i && rows > 0) {
-            const int64_t src = unit * (static_cast<int64_t>(P) * D) + (tok & (P - 1)) * D;
-            const uint32_t dst = stage0 + stage * S::kStage + 16 * g * D;
-            bulk_load(dst, a.pool.k + src, rows * D, bar);
-            bulk_load(dst + kTile * D, a.pool.v + src, rows * D, bar);
-          }
-          ++issued;
-          if (++stage == NS) {
-            stage = 0;
-            phase ^= 1;
-          }
+        __syncwarp();
+        if (lane == 4 * i) tma::mbar_arrive(bar);
+        ++issued;
+        if (++stage == NS) {
+          stage = 0;
+          phase ^= 1;
         }
       }
+      now = look(w + 8);  // with this batch's last copies in flight
     }
     // no copy is left in flight when the CTA ends
     const int last = min(issued, NS);
@@ -321,41 +308,86 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? 2 : 1) attend_rows_kernel(
 
   // ---- consumers
   const int g = lane >> 2, t = lane & 3;
-  int stage = 0, phase = 0;
-  bool dead = false;
-  for (int64_t w = run.lo; w < run.hi;) {
+  constexpr int VW = D >= 128 ? 4 : 2;  // words of a token's values that a thread reads at once
+  constexpr int H = D / (32 * VW);
+
+  struct Segment {
+    int64_t w;        // its first place
     int64_t lh;
-    int32_t bi, t0, nt;
-    bool whole;
-    segment(w, lh, bi, t0, nt, whole);
-    const bool at_start = w == run.lo;
-    w += nt;
-    bool ignored = false;
-    const Item it = find_item<R>(a, bi, &ignored);
-    const int l = static_cast<int>(lh / a.pool.hk), h = static_cast<int>(lh - l * a.pool.hk);
+    int32_t entry;
+    int32_t t0, nt;   // tiles
+    bool whole, late; // the whole item; the item started before this run
+  };
+  // The first segment at or behind place w; nt = 0 behind the last.
+  auto segment = [&](int64_t w) {
+    Segment sg{w, 0, 0, 0, 0, false, false};
+    while (sg.w < run_hi) {
+      const int64_t lh = sg.w / total;
+      const int32_t r = static_cast<int32_t>(sg.w - lh * total);
+      const int32_t e = entry_at(r);
+      const int64_t start = lh * total + s_prefix[e], end = lh * total + s_prefix[e + 1];
+      const int64_t lo = max(sg.w, start + kLead), hi = min(end, run_hi);
+      if (lo < hi) {
+        sg.lh = lh + lh0;
+        sg.entry = e;
+        sg.t0 = static_cast<int32_t>(lo - start) - kLead;
+        sg.nt = static_cast<int32_t>(hi - lo);
+        sg.whole = sg.t0 == 0 && hi == end;
+        sg.late = start < run_lo;
+        sg.w = hi;  // where the next begins
+        return sg;
+      }
+      sg.w = min(end, run_hi);
+    }
+    return sg;
+  };
+  // Element offset of query row r of an item.
+  auto row_at = [&](const Item& it, int l, int h, int r) {
+    const int f = it.first_row + r;
+    const int64_t tok = it.tok + f / a.group;
+    return ((l * a.batch.n_tokens + tok) * a.hq + h * a.group + f % a.group) * D;
+  };
+  constexpr int kPer = kConsumers / R;                            // threads of a row of Q
+  constexpr int kHave = D / 8 / kPer > 0 ? D / 8 / kPer : 1;      // 16-byte chunks of a thread
+  const int q_row = tid / kPer, q_chunk = tid % kPer;
+  auto load_q = [&](const Item& it, int l, int h, uint4 (&x)[kHave]) {
+#pragma unroll
+    for (int k = 0; k < kHave; ++k) {
+      x[k] = make_uint4(0, 0, 0, 0);
+      const int c = q_chunk + k * kPer;
+      if (q_row < it.rows && c < D / 8)
+        x[k] = __ldg(reinterpret_cast<const uint4*>(a.q + row_at(it, l, h, q_row)) + c);
+    }
+  };
+
+  int stage = 0, phase = 0, turn = 0;
+  bool dead = false, ignored = false;
+  Segment sg = segment(run_lo);
+  int4 left = make_int4(-1, 0, 0, 0);
+  Item it{};
+  int l = 0, h = 0;
+  uint4 xq[kHave];
+  if (sg.nt > 0) {
+    l = static_cast<int>(sg.lh / a.pool.hk);
+    h = static_cast<int>(sg.lh - static_cast<int64_t>(l) * a.pool.hk);
+    it = find_item<R>(a, first + sg.entry, &ignored);
+    load_q(it, l, h, xq);
+  }
+  while (sg.nt > 0) {
     const int vis_first = static_cast<int>(it.vis_first), vis_last = static_cast<int>(it.vis_last);
-    auto row_at = [&](int r) {  // element offset of query row r of the item
-      const int f = it.first_row + r;
-      const int64_t tok = it.tok + f / a.group;
-      const int head = h * a.group + f % a.group;
-      return ((l * a.batch.n_tokens + tok) * a.hq + head) * D;
-    };
+    turn ^= 1;  // the rows' words have two places: the last segment's may still be read
+    int* s_nan = reinterpret_cast<int*>(smem + S::kNan) + turn * D;
+    float* s_mult = reinterpret_cast<float*>(smem + S::kRow) + turn * S::kRowWords;  // [R]
+    int* s_vis = reinterpret_cast<int*>(s_mult + R);  // [R] tokens seen
+    float* s_ref = reinterpret_cast<float*>(s_vis + R);  // [warps][R]
+    float* s_sum = s_ref + kWarps * R;                   // [warps][R]
 
     // Q to f16, each row over a power of two, in the order of the B fragments
     {
-      constexpr int kPer = kConsumers / R;       // threads of a row
-      constexpr int kChunks = D / 8 / kPer;      // 16-byte chunks of a thread (>= 1)
-      constexpr int kHave = kChunks > 0 ? kChunks : 1;
-      const int r = tid / kPer, c0 = tid % kPer;
-      uint4 x[kHave];
       uint32_t mx = 0;
 #pragma unroll
       for (int k = 0; k < kHave; ++k) {
-        x[k] = make_uint4(0, 0, 0, 0);
-        const int c = c0 + k * kPer;
-        if (r < it.rows && c < D / 8)
-          x[k] = __ldg(reinterpret_cast<const uint4*>(a.q + row_at(r)) + c);
-        const uint32_t ww[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+        const uint32_t ww[4] = {xq[k].x, xq[k].y, xq[k].z, xq[k].w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) mx = __vmaxs2(mx, ww[i] & 0x7fff7fffu);
       }
@@ -368,32 +400,42 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? 2 : 1) attend_rows_kernel(
       const float inv = __int_as_float((127 - e) << 23);
 #pragma unroll
       for (int k = 0; k < kHave; ++k) {
-        const int c = c0 + k * kPer;
+        const int c = q_chunk + k * kPer;
         if (c < D / 8) {
-          const uint32_t ww[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+          const uint32_t ww[4] = {xq[k].x, xq[k].y, xq[k].z, xq[k].w};
           uint32_t f[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             f[i] = finite ? pack_f16x2(bf16_lo(ww[i]) * inv, bf16_hi(ww[i]) * inv) : 0x7fff7fffu;
           const int d = 8 * c;
           const int m = d / 64 * 4 + (d % 16) / 4, tt = (d % 64) / 16;
-          const int nq = r / 8, gq = r % 8;
+          const int nq = q_row / 8, gq = q_row % 8;
           s_q[(m * NQ + nq) * 32 + gq * 4 + tt] = make_uint2(f[0], f[1]);
           s_q[((m + 1) * NQ + nq) * 32 + gq * 4 + tt] = make_uint2(f[2], f[3]);
         }
       }
-      if (c0 == 0) {
-        s_mult[r] = a.scale_log2 * __int_as_float((127 + e) << 23);
-        const int64_t seen = it.p0 + (it.first_row + r) / a.group + 1;
-        s_vis[r] = r < it.rows ? static_cast<int>(max(static_cast<int64_t>(0),
-                                                      min(seen, it.vis_last)))
-                               : 0;
+      if (q_chunk == 0) {
+        s_mult[q_row] = a.scale_log2 * __int_as_float((127 + e) << 23);
+        const int64_t seen = it.p0 + (it.first_row + q_row) / a.group + 1;
+        s_vis[q_row] = q_row < it.rows ? static_cast<int>(max(static_cast<int64_t>(0),
+                                                              min(seen, it.vis_last)))
+                                       : 0;
       }
       for (int d = tid; d < D; d += kConsumers) s_nan[d] = 0x7fffffff;
     }
+    // the next segment's Q is on its way during this one's tiles
+    const Segment next = segment(sg.w);
+    Item next_it{};
+    int next_l = 0, next_h = 0;
+    if (next.nt > 0) {
+      next_l = static_cast<int>(next.lh / a.pool.hk);
+      next_h = static_cast<int>(next.lh - static_cast<int64_t>(next_l) * a.pool.hk);
+      next_it = find_item<R>(a, first + next.entry, &ignored);
+      load_q(next_it, next_l, next_h, xq);
+    }
     tma::named_sync(1, kConsumers);
 
-    float o[D / 16][NQ][4];
+    float o[M][NQ][4];
     float ref[NQ][2], sum[NQ][2], mult[NQ][2];
     int vis[NQ][2];
 #pragma unroll
@@ -406,28 +448,33 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? 2 : 1) attend_rows_kernel(
         vis[n][i] = s_vis[8 * n + 2 * t + i];
       }
 #pragma unroll
-      for (int m = 0; m < D / 16; ++m)
+      for (int m = 0; m < M; ++m)
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[m][n][i] = 0.f;
     }
 
-    for (int tile = 0; tile < nt; ++tile) {
+    uint8_t* used = nullptr;  // the last tile's stage
+    for (int tile = 0; tile < sg.nt; ++tile) {
       if (!dead && !tma::mbar_wait(full0 + 8 * stage, phase, tma::kConsumerWaitLimitNs)) dead = true;
-      const uint8_t* kt = smem + stage * S::kStage + warp * 16 * D;
+      used = smem + stage * S::kStage;
+      const uint8_t* kt = used + warp * 16 * D;
       const uint8_t* vt = kt + kTile * D;
       const StageInfo& info = s_info[stage];
       const float k_scale = info.k_scale[warp], v_log2 = info.v_log2[warp];
       const float v_inv = info.v_inv[warp];
-      const bool valid = (info.valid >> warp) & 1u;
-      const int tok0 = (t0 + tile) * kTile + warp * 16;
+      const int tok0 = (sg.t0 + tile) * kTile + warp * 16;
+      const bool live = ((info.valid >> warp) & 1u) && tok0 < vis_last;
 
-      // scores of tokens tok0 + g and + g + 8 against queries 2t, 2t + 1
-      float s[NQ][4];
+      if (live) {
+        // scores of tokens tok0 + g and + g + 8 against queries 2t, 2t + 1, summed
+        // over the dims in four chains
+        float part[4][NQ][4];
 #pragma unroll
-      for (int n = 0; n < NQ; ++n)
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[n][i] = 0.f;
-      if (valid && tok0 < vis_last) {
+          for (int n = 0; n < NQ; ++n)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) part[i][n][x] = 0.f;
 #pragma unroll
         for (int j = 0; j < D / 64; ++j) {
           const uint4 lo = *reinterpret_cast<const uint4*>(kt + g * D + j * 64 + t * 16);
@@ -440,69 +487,67 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? 2 : 1) attend_rows_kernel(
 #pragma unroll
             for (int n = 0; n < NQ; ++n) {
               const uint2 q = s_q[((j * 4 + i) * NQ + n) * 32 + lane];
-              mma_f16(s[n], a0, a1, a2, a3, q.x, q.y);
+              mma_f16(part[i][n], a0, a1, a2, a3, q.x, q.y);
             }
           }
         }
-      }
-      uint32_t pb[NQ][2];
-      bool move = false;
-      float mx[NQ][2];
-#pragma unroll
-      for (int n = 0; n < NQ; ++n) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int tok = tok0 + g + (i >= 2 ? 8 : 0);
-          const float x = fmaf(s[n][i], mult[n][i & 1] * k_scale, v_log2);
-          s[n][i] = valid && tok < vis[n][i & 1] ? x : -INFINITY;
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          float m = fmaxf(s[n][i], s[n][i + 2]);
-          m = fmaxf(m, __shfl_xor_sync(~0u, m, 4));
-          m = fmaxf(m, __shfl_xor_sync(~0u, m, 8));
-          m = fmaxf(m, __shfl_xor_sync(~0u, m, 16));
-          mx[n][i] = m;
-          move |= m > ref[n][i] + kLazy;
-        }
-      }
-      if (__any_sync(~0u, move)) {
+        float s[NQ][4];
+        uint32_t pb[NQ][2];
+        bool move = false;
+        float mx[NQ][2];
 #pragma unroll
         for (int n = 0; n < NQ; ++n) {
-          float f[2];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int tok = tok0 + g + (i >= 2 ? 8 : 0);
+            const float dot = (part[0][n][i] + part[1][n][i]) + (part[2][n][i] + part[3][n][i]);
+            const float x = fmaf(dot, mult[n][i & 1] * k_scale, v_log2);
+            s[n][i] = tok < vis[n][i & 1] ? x : -INFINITY;
+          }
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const float r = fmaxf(ref[n][i], mx[n][i]);
-            f[i] = r == -INFINITY ? 1.f : exp2_approx(ref[n][i] - r);
-            ref[n][i] = r;
-            sum[n][i] *= f[i];
-          }
-#pragma unroll
-          for (int m = 0; m < D / 16; ++m) {
-            o[m][n][0] *= f[0];
-            o[m][n][1] *= f[1];
-            o[m][n][2] *= f[0];
-            o[m][n][3] *= f[1];
+            float m = fmaxf(s[n][i], s[n][i + 2]);
+            m = fmaxf(m, __shfl_xor_sync(~0u, m, 4));
+            m = fmaxf(m, __shfl_xor_sync(~0u, m, 8));
+            m = fmaxf(m, __shfl_xor_sync(~0u, m, 16));
+            mx[n][i] = m;
+            move |= m > ref[n][i] + kLazy;
           }
         }
-      }
+        if (__any_sync(~0u, move)) {
 #pragma unroll
-      for (int n = 0; n < NQ; ++n) {
-        float p[4];
+          for (int n = 0; n < NQ; ++n) {
+            float f[2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float r = ref[n][i & 1] == -INFINITY ? 0.f : ref[n][i & 1];
-          p[i] = exp2_approx(s[n][i] - r);
-          sum[n][i & 1] = fmaf(p[i], v_inv, sum[n][i & 1]);
+            for (int i = 0; i < 2; ++i) {
+              const float r = fmaxf(ref[n][i], mx[n][i]);
+              f[i] = r == -INFINITY ? 1.f : exp2_approx(ref[n][i] - r);
+              ref[n][i] = r;
+              sum[n][i] *= f[i];
+            }
+#pragma unroll
+            for (int m = 0; m < M; ++m) {
+              o[m][n][0] *= f[0];
+              o[m][n][1] *= f[1];
+              o[m][n][2] *= f[0];
+              o[m][n][3] *= f[1];
+            }
+          }
         }
-        pb[n][0] = transpose_8x8(pack_f16x2(p[0], p[1]));
-        pb[n][1] = transpose_8x8(pack_f16x2(p[2], p[3]));
-      }
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) {
+          float p[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float r = ref[n][i & 1] == -INFINITY ? 0.f : ref[n][i & 1];
+            p[i] = exp2_approx(s[n][i] - r);
+            sum[n][i & 1] = fmaf(p[i], v_inv, sum[n][i & 1]);
+          }
+          pb[n][0] = transpose_8x8(pack_f16x2(p[0], p[1]));
+          pb[n][1] = transpose_8x8(pack_f16x2(p[2], p[3]));
+        }
 
-      // O^T += V^T P^T over the 16 tokens
-      if (valid && tok0 < vis_last) {
-        constexpr int VW = D >= 128 ? 4 : 2;  // words of a token that a thread reads at once
-        constexpr int H = D / (32 * VW);
+        // O^T += V^T P^T over the 16 tokens
         const bool edge = tok0 + 16 > vis_first;  // some row does not see all of them
 #pragma unroll
         for (int hh = 0; hh < H; ++hh) {
@@ -569,14 +614,16 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? 2 : 1) attend_rows_kernel(
         }
       }
       __syncwarp();
-      if (lane == 0) tma::mbar_arrive(empty0 + 8 * stage);
-      if (++stage == NS) {
-        stage = 0;
-        phase ^= 1;
+      if (tile + 1 < sg.nt) {  // the last tile's stage is kept for the joining below
+        if (lane == 0) tma::mbar_arrive(empty0 + 8 * stage);
+        if (++stage == NS) {
+          stage = 0;
+          phase ^= 1;
+        }
       }
     }
 
-    // join the four warps, one after another
+    // join the four warps through the last tile's stage
 #pragma unroll
     for (int n = 0; n < NQ; ++n)
 #pragma unroll
@@ -590,109 +637,196 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? 2 : 1) attend_rows_kernel(
           s_sum[warp * R + 8 * n + 2 * t + i] = x;
         }
       }
-    tma::named_sync(1, kConsumers);
-    float f[NQ][2];
+    tma::named_sync(1, kConsumers);  // the tile has been read by all
+    float4* dump = reinterpret_cast<float4*>(used);
+    constexpr int kSlots = M * NQ * 32;  // of a warp's O
+    constexpr int kDumps = 8 / (2 * NQ);  // warps whose O a stage holds: 4 or 2
+    {
+      float f[NQ][2];
 #pragma unroll
-    for (int n = 0; n < NQ; ++n)
+      for (int n = 0; n < NQ; ++n)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int r = 8 * n + 2 * t + i;
+          float top = s_ref[r];
+#pragma unroll
+          for (int k = 1; k < kWarps; ++k) top = fmaxf(top, s_ref[k * R + r]);
+          f[n][i] = top == -INFINITY ? 1.f : exp2_approx(ref[n][i] - top);
+        }
+#pragma unroll
+      for (int m = 0; m < M; ++m)
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) {
+          o[m][n][0] *= f[n][0];
+          o[m][n][1] *= f[n][1];
+          o[m][n][2] *= f[n][0];
+          o[m][n][3] *= f[n][1];
+        }
+    }
+    if constexpr (kDumps < kWarps) {  // the upper warps' first, into the lower ones
+      if (warp >= kDumps)
+#pragma unroll
+        for (int m = 0; m < M; ++m)
+#pragma unroll
+          for (int n = 0; n < NQ; ++n)
+            dump[(warp - kDumps) * kSlots + (m * NQ + n) * 32 + lane] =
+                make_float4(o[m][n][0], o[m][n][1], o[m][n][2], o[m][n][3]);
+      tma::named_sync(1, kConsumers);
+      if (warp < kDumps)
+#pragma unroll
+        for (int m = 0; m < M; ++m)
+#pragma unroll
+          for (int n = 0; n < NQ; ++n) {
+            const float4 x = dump[warp * kSlots + (m * NQ + n) * 32 + lane];
+            o[m][n][0] += x.x;
+            o[m][n][1] += x.y;
+            o[m][n][2] += x.z;
+            o[m][n][3] += x.w;
+          }
+      tma::named_sync(1, kConsumers);
+    }
+    if (warp < kDumps)
+#pragma unroll
+      for (int m = 0; m < M; ++m)
+#pragma unroll
+        for (int n = 0; n < NQ; ++n)
+          dump[warp * kSlots + (m * NQ + n) * 32 + lane] =
+              make_float4(o[m][n][0], o[m][n][1], o[m][n][2], o[m][n][3]);
+    tma::named_sync(1, kConsumers);
+    // thread (warp, lane) finishes blocks m of its warp's quarter: consecutive dims
+    // of queries 2t and 2t + 1
+    constexpr int kMine = M / kWarps;
+    float* rec = ra.partial + (static_cast<int64_t>(blockIdx.x) * 2 + (sg.late ? 0 : 1)) *
+                                  (R * (D + 2));
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+      float y[2][2 * kMine];
+#pragma unroll
+      for (int k = 0; k < kMine; ++k) {
+        const int slot = ((warp * kMine + k) * NQ + n) * 32 + lane;
+        float4 x = dump[slot];
+#pragma unroll
+        for (int w = 1; w < kDumps; ++w) {
+          const float4 z = dump[w * kSlots + slot];
+          x.x += z.x;
+          x.y += z.y;
+          x.z += z.z;
+          x.w += z.w;
+        }
+        y[0][2 * k] = x.x;
+        y[1][2 * k] = x.y;
+        y[0][2 * k + 1] = x.z;
+        y[1][2 * k + 1] = x.w;
+      }
+      const int m0 = warp * kMine;
+      const int d = m0 / (2 * VW) * 32 * VW + g * 4 * VW + 2 * (m0 % (2 * VW));
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int r = 8 * n + 2 * t + i;
+        if (r >= it.rows) continue;
         float top = s_ref[r];
 #pragma unroll
         for (int k = 1; k < kWarps; ++k) top = fmaxf(top, s_ref[k * R + r]);
-        f[n][i] = top == -INFINITY ? 0.f : exp2_approx(ref[n][i] - top);
-      }
-    for (int turn = 0; turn < kWarps; ++turn) {
-      if (warp == turn) {
-        constexpr int VW = D >= 128 ? 4 : 2;
-#pragma unroll
-        for (int m = 0; m < D / 16; ++m) {
-          const int d = (m / (2 * VW)) * 32 * VW + g * 4 * VW + 2 * (m % (2 * VW));
-#pragma unroll
-          for (int n = 0; n < NQ; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              float* dst = s_o + (8 * n + 2 * t + (i & 1)) * (D + 4) + d + (i >> 1);
-              const float x = o[m][n][i] * f[n][i & 1];
-              *dst = turn == 0 ? x : *dst + x;
-            }
-        }
-      }
-      tma::named_sync(1, kConsumers);
-    }
-    for (int idx = tid; idx < R * (D / 4); idx += kConsumers) {
-      const int r = idx / (D / 4), d = (idx - r * (D / 4)) * 4;
-      if (r >= it.rows) continue;
-      float top = s_ref[r];
-#pragma unroll
-      for (int k = 1; k < kWarps; ++k) top = fmaxf(top, s_ref[k * R + r]);
-      float total = 0.f;
-      if (top != -INFINITY)
+        float all = 0.f;
 #pragma unroll
         for (int k = 0; k < kWarps; ++k)
-          total += s_sum[k * R + r] * exp2_approx(s_ref[k * R + r] - top);
-      float4 x = *reinterpret_cast<const float4*>(s_o + r * (D + 4) + d);
-      const int4 from = *reinterpret_cast<const int4*>(s_nan + d);
-      const int seen = s_vis[r];
-      const float nan = __int_as_float(0x7fffffff);
-      if (from.x < seen) x.x = nan;
-      if (from.y < seen) x.y = nan;
-      if (from.z < seen) x.z = nan;
-      if (from.w < seen) x.w = nan;
-      if (whole) {
-        const float inv = total == 0.f ? 0.f : 1.f / total;
-        *reinterpret_cast<uint2*>(a.out + row_at(r) + d) =
-            make_uint2(pack_bf16x2(x.x * inv, x.y * inv), pack_bf16x2(x.z * inv, x.w * inv));
-      } else {
-        float* rec = ra.partial + (static_cast<int64_t>(blockIdx.x) * 2 + (at_start ? 0 : 1)) *
-                                      (R * (D + 2));
-        *reinterpret_cast<float4*>(rec + r * D + d) = x;
-        if (d == 0) {
-          rec[R * D + r] = top;
-          rec[R * D + R + r] = total;
+          all += s_sum[k * R + r] * (top == -INFINITY ? 1.f : exp2_approx(s_ref[k * R + r] - top));
+        const int seen = s_vis[r];
+#pragma unroll
+        for (int k = 0; k < 2 * kMine; ++k)
+          if (s_nan[d + k] < seen) y[i][k] = __int_as_float(0x7fffffff);
+        if (sg.whole) {
+          const float inv = all == 0.f ? 0.f : 1.f / all;
+          uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + row_at(it, l, h, r) + d);
+          uint32_t w[kMine];
+#pragma unroll
+          for (int k = 0; k < kMine; ++k) w[k] = pack_bf16x2(y[i][2 * k] * inv, y[i][2 * k + 1] * inv);
+          if constexpr (kMine == 4)
+            *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+          else
+#pragma unroll
+            for (int k = 0; k < kMine; ++k) dst[k] = w[k];
+        } else {
+#pragma unroll
+          for (int k = 0; k < kMine; ++k)
+            *reinterpret_cast<float2*>(rec + r * D + d + 2 * k) =
+                make_float2(y[i][2 * k], y[i][2 * k + 1]);
+          if (d == 0) {
+            rec[R * D + r] = top;
+            rec[R * D + R + r] = all;
+          }
         }
       }
     }
-    tma::named_sync(1, kConsumers);  // Q, rows and O are rewritten for the next segment
+    if (!sg.whole && sg.t0 == 0) {  // the run's last: it goes on in the next
+      const int64_t end = (sg.lh - lh0) * total + s_prefix[sg.entry + 1];
+      left = make_int4(static_cast<int>(sg.lh), sg.entry,
+                       static_cast<int>((end - 1) / max(run_hi - run_lo, static_cast<int64_t>(1))),
+                       sg.late ? 0 : 1);
+    }
+    // the stage goes back: plain accesses before the next copy into it
+    tma::fence_async_shared();
+    __syncwarp();
+    if (lane == 0) tma::mbar_arrive(empty0 + 8 * stage);
+    if (++stage == NS) {
+      stage = 0;
+      phase ^= 1;
+    }
+    sg = next;
+    it = next_it;
+    l = next_l;
+    h = next_h;
   }
+  if (tid == 0 && ra.ctas > 0) ra.left[blockIdx.x] = left;
   if (dead && lane == 0 && a.status != nullptr) atomicOr(a.status, CMR_DEVICE_WAIT_TIMEOUT);
 }
 
 constexpr int kJoinThreads = 256;
+constexpr int kJoinLanes = 16;                          // threads of 64 dims of a row
+constexpr int kJoinGroups = kJoinThreads / kJoinLanes;  // partial results read at once
+constexpr int kJoinAhead = 8;                           // and ahead by each thread
 
-// Joins the partial results of an item's row: grid (items x layers x heads, R).
+// Joins the partial results of 64 dims of an item's row: grid (items x layers x
+// heads, R, D / 64).
 template <int D, int NQ>
 __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const RowsArgs ra) {
   constexpr int R = 8 * NQ;
-  constexpr int kLanes = D / 4;                    // threads of a row of a partial result
-  constexpr int kGroups = kJoinThreads / kLanes;
   __shared__ float s_w[kMaxCtas];
   __shared__ float s_red[2][kJoinThreads / 32];
   __shared__ float4 s_o[kJoinThreads];
   const AttendArgs& a = ra.a;
-  pdl::wait();
   const int tid = threadIdx.x;
   const int32_t NB = ra.items;
   const int32_t bi = static_cast<int32_t>(blockIdx.x % NB);
   const int64_t lh = blockIdx.x / NB;
-  const int64_t total = __ldcg(ra.prefix + NB);
-  const int64_t lo = lh * total + __ldcg(ra.prefix + bi);
-  const int64_t hi = lh * total + __ldcg(ra.prefix + bi + 1);
-  if (lo >= hi) return;
-  const int64_t all = total * a.pool.num_layers * a.pool.hk;
-  const int64_t per = (all + ra.ctas - 1) / ra.ctas;
-  const int64_t c0 = lo / per, c1 = (hi - 1) / per;
-  if (c0 == c1) return;  // written whole
   bool bad = false;
-  const Item it = find_item<R>(a, bi, &bad);
+  const Item it = find_item<R>(a, bi, &bad);  // of the call's inputs: no need to wait
   const int r = blockIdx.y;
   if (r >= it.rows) return;
+  pdl::wait();
+  const int64_t total = __ldcg(ra.prefix + NB);
+  const int64_t start = lh * total + __ldcg(ra.prefix + bi);
+  const int64_t end = lh * total + __ldcg(ra.prefix + bi + 1);
+  const int64_t all = total * a.pool.num_layers * a.pool.hk;
+  const int64_t per = (all + ra.ctas - 1) / ra.ctas;
+  const int64_t c0 = (start + kLead) / per, c1 = (end - 1) / per;
+  if (c0 == c1) return;  // written whole
   const int n = static_cast<int>(c1 - c0 + 1);
   constexpr int kRec = R * (D + 2);
-  auto record = [&](int k) {  // the item starts inside CTA c0's run unless at its start
+  auto record = [&](int k) {  // in the second place where the item starts within the run
     const int64_t c = c0 + k;
-    return ra.partial + (c * 2 + (c * per >= lo ? 0 : 1)) * kRec;
+    return ra.partial + (c * 2 + (start >= c * per ? 1 : 0)) * kRec;
   };
+  const int ln = tid % kJoinLanes, gr = tid / kJoinLanes;
+  const int d = blockIdx.z * 4 * kJoinLanes + 4 * ln;
+  // the first values are on their way while their weights are found
+  float4 x[kJoinAhead];
+#pragma unroll
+  for (int i = 0; i < kJoinAhead; ++i) {
+    const int k = gr + i * kJoinGroups;
+    x[i] = k < n ? __ldcg(reinterpret_cast<const float4*>(record(k) + r * D + d))
+                 : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
   float top = -INFINITY;
   for (int k = tid; k < n; k += kJoinThreads) {
     const float m = __ldcg(record(k) + R * D + r);
@@ -707,7 +841,7 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const RowsArg
   for (int k = 0; k < kJoinThreads / 32; ++k) top = fmaxf(top, s_red[0][k]);
   float sum = 0.f;
   for (int k = tid; k < n; k += kJoinThreads) {
-    const float w = top == -INFINITY ? 0.f : exp2_approx(s_w[k] - top);
+    const float w = top == -INFINITY ? 1.f : exp2_approx(s_w[k] - top);
     s_w[k] = w;
     sum += w * __ldcg(record(k) + R * D + R + r);
   }
@@ -718,33 +852,83 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const RowsArg
   sum = 0.f;
 #pragma unroll
   for (int k = 0; k < kJoinThreads / 32; ++k) sum += s_red[1][k];
-  const int ln = tid % kLanes, gr = tid / kLanes;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int k = gr; k < n; k += kGroups) {
-    const float4 x = __ldcg(reinterpret_cast<const float4*>(record(k) + r * D) + ln);
-    const float w = s_w[k];
-    acc.x = fmaf(w, x.x, acc.x);
-    acc.y = fmaf(w, x.y, acc.y);
-    acc.z = fmaf(w, x.z, acc.z);
-    acc.w = fmaf(w, x.w, acc.w);
+  auto add = [&](float w, const float4& y) {
+    acc.x = fmaf(w, y.x, acc.x);
+    acc.y = fmaf(w, y.y, acc.y);
+    acc.z = fmaf(w, y.z, acc.z);
+    acc.w = fmaf(w, y.w, acc.w);
+  };
+#pragma unroll
+  for (int i = 0; i < kJoinAhead; ++i) {
+    const int k = gr + i * kJoinGroups;
+    if (k < n) add(s_w[k], x[i]);
   }
+  for (int k = gr + kJoinAhead * kJoinGroups; k < n; k += kJoinGroups)
+    add(s_w[k], __ldcg(reinterpret_cast<const float4*>(record(k) + r * D + d)));
   s_o[tid] = acc;
   __syncthreads();
   if (gr == 0) {
 #pragma unroll
-    for (int k = 1; k < kGroups; ++k) {
-      const float4 x = s_o[k * kLanes + ln];
-      acc.x += x.x;
-      acc.y += x.y;
-      acc.z += x.z;
-      acc.w += x.w;
+    for (int k = 1; k < kJoinGroups; ++k) {
+      const float4 y = s_o[k * kJoinLanes + ln];
+      acc.x += y.x;
+      acc.y += y.y;
+      acc.z += y.z;
+      acc.w += y.w;
     }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    const int l = static_cast<int>(lh / a.pool.hk), h = static_cast<int>(lh - l * a.pool.hk);
+    const int l = static_cast<int>(lh / a.pool.hk);
+    const int h = static_cast<int>(lh - static_cast<int64_t>(l) * a.pool.hk);
     const int f = it.first_row + r;
     uint16_t* dst = a.out + ((l * a.batch.n_tokens + it.tok + f / a.group) * a.hq + h * a.group +
-                             f % a.group) * D + 4 * ln;
+                             f % a.group) * D + d;
+    *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv),
+                                                pack_bf16x2(acc.z * inv, acc.w * inv));
+  }
+}
+
+// The same with a CTA for each run, for calls of many items: each run leaves at
+// most one item to be joined, of a few pieces.
+template <int D, int NQ>
+__global__ void __launch_bounds__(kJoinThreads) attend_join_runs_kernel(const RowsArgs ra) {
+  constexpr int R = 8 * NQ;
+  constexpr int kRec = R * (D + 2);
+  const AttendArgs& a = ra.a;
+  pdl::wait();
+  const int4 left = __ldcg(ra.left + blockIdx.x);
+  if (left.x < 0) return;
+  const int64_t lh = left.x;
+  const int c0 = blockIdx.x, c1 = left.z;
+  const float* rec0 = ra.partial + (static_cast<int64_t>(c0) * 2 + left.w) * kRec;
+  bool bad = false;
+  const Item it = find_item<R>(a, left.y, &bad);
+  const int l = static_cast<int>(lh / a.pool.hk);
+  const int h = static_cast<int>(lh - static_cast<int64_t>(l) * a.pool.hk);
+  for (int idx = threadIdx.x; idx < it.rows * (D / 4); idx += kJoinThreads) {
+    const int r = idx / (D / 4), d = (idx - r * (D / 4)) * 4;
+    float top = __ldcg(rec0 + R * D + r);
+    float sum = __ldcg(rec0 + R * D + R + r);
+    float4 acc = __ldcg(reinterpret_cast<const float4*>(rec0 + r * D + d));
+#pragma unroll 4
+    for (int c = c0 + 1; c <= c1; ++c) {
+      const float* rec = ra.partial + static_cast<int64_t>(c) * 2 * kRec;
+      const float ref = __ldcg(rec + R * D + r);
+      const float4 x = __ldcg(reinterpret_cast<const float4*>(rec + r * D + d));
+      const float to = fmaxf(top, ref);
+      const float f = to == -INFINITY ? 1.f : exp2_approx(top - to);
+      const float w = to == -INFINITY ? 1.f : exp2_approx(ref - to);
+      top = to;
+      sum = fmaf(sum, f, w * __ldcg(rec + R * D + R + r));
+      acc.x = fmaf(acc.x, f, w * x.x);
+      acc.y = fmaf(acc.y, f, w * x.y);
+      acc.z = fmaf(acc.z, f, w * x.z);
+      acc.w = fmaf(acc.w, f, w * x.w);
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const int f = it.first_row + r;
+    uint16_t* dst = a.out + ((l * a.batch.n_tokens + it.tok + f / a.group) * a.hq + h * a.group +
+                             f % a.group) * D + d;
     *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv),
                                                 pack_bf16x2(acc.z * inv, acc.w * inv));
   }
@@ -765,10 +949,10 @@ cudaError_t launch(RowsArgs ra, cudaStream_t stream) {
   using S = Smem<D, NQ>;
   const AttendArgs& a = ra.a;
   const int64_t lh = static_cast<int64_t>(a.pool.num_layers) * a.pool.hk;
-  const size_t smem = S::kPrefix + (ra.ctas > 0 ? (ra.items + 1) * sizeof(int) : 0);
+  const size_t smem = S::kItems + (3 * (ra.ctas > 0 ? ra.items : 1) + 1) * sizeof(int);
   cudaError_t e = cudaFuncSetAttribute(
       attend_rows_kernel<D, NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-      static_cast<int>(S::kPrefix + (kMaxSplitItems + 1) * sizeof(int)));
+      static_cast<int>(S::kItems + (3 * kMaxSplitItems + 1) * sizeof(int)));
   if (e != cudaSuccess) return e;
   if (ra.ctas == 0) {
     if (lh > 65535) return cudaErrorInvalidValue;
@@ -778,8 +962,16 @@ cudaError_t launch(RowsArgs ra, cudaStream_t stream) {
   attend_rows_kernel<D, NQ><<<ra.ctas, kThreads, smem, stream>>>(ra);
   e = cudaGetLastError();
   if (e != cudaSuccess || ra.ctas == 1) return e;
-  return pdl::launch(attend_join_kernel<D, NQ>, dim3(static_cast<unsigned>(ra.items * lh), 8 * NQ),
-                     dim3(kJoinThreads), 0, stream, true, ra);
+  // With one item to four runs or more, an item is cut into a few pieces: a CTA
+  // joins them all.  With fewer items there are many pieces, and the CTAs share
+  // an item's rows and dims.
+  if (ra.items * lh * 4 >= ra.ctas)
+    return pdl::launch(attend_join_runs_kernel<D, NQ>, dim3(ra.ctas), dim3(kJoinThreads), 0, stream,
+                       true, ra);
+  const int rows = a.batch.cu == nullptr && a.group < 8 * NQ ? a.group : 8 * NQ;
+  return pdl::launch(attend_join_kernel<D, NQ>,
+                     dim3(static_cast<unsigned>(ra.items * lh), rows, D / 64), dim3(kJoinThreads),
+                     0, stream, true, ra);
 }
 
 }  // namespace
@@ -794,6 +986,7 @@ size_t attend_rows_workspace(int32_t num_seqs, int64_t n_tokens, int32_t hq, int
     const int64_t nb = item_slots(num_seqs, n_tokens, group, R, step);
     if (nb > kMaxSplitItems) continue;
     const size_t bytes = align16((nb + 1) * sizeof(int32_t)) +
+                         static_cast<size_t>(max_ctas(R)) * sizeof(int4) +
                          static_cast<size_t>(max_ctas(R)) * 2 * R * (head_dim + 2) * sizeof(float);
     most = bytes > most ? bytes : most;
   }
@@ -809,11 +1002,12 @@ cudaError_t launch_attend_rows(const AttendArgs& a, cudaStream_t stream) {
   ra.a = a;
   ra.items = static_cast<int32_t>(nb);
   const int64_t cap = static_cast<int64_t>(a.table.max_pages) << a.pool.page_shift;
-  const int64_t most_tiles = (cap + kTile - 1) / kTile * nb;  // per layer and head
+  const int64_t most_tiles = ((cap + kTile - 1) / kTile + kLead) * nb;  // per layer and head
   if (nb <= kMaxSplitItems && most_tiles <= INT32_MAX) {
     ra.prefix = static_cast<int32_t*>(a.workspace);
-    ra.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) +
-                                          align16((nb + 1) * sizeof(int32_t)));
+    ra.left = reinterpret_cast<int4*>(static_cast<uint8_t*>(a.workspace) +
+                                      align16((nb + 1) * sizeof(int32_t)));
+    ra.partial = reinterpret_cast<float*>(ra.left + max_ctas(R));
     // no more CTAs than there can be tiles
     const int64_t tiles = most_tiles * a.pool.num_layers * a.pool.hk;
     const int most = max_ctas(R);

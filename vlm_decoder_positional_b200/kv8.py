@@ -19,7 +19,7 @@ from typing import Optional, Sequence, Tuple
 
 import torch
 
-from .cmr import CMR_OK, _stream_ptr
+from .cmr import CMR_OK
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libcmr_kv8.so")
@@ -45,7 +45,7 @@ SIGNATURES = {
     "cmr_kv8_extend": (ctypes.c_int, [_p, _i, _i, _p, _i, _i, _p, _p, _i, _p, _z, _p, _p]),
     "cmr_kv8_fork": (ctypes.c_int, _POOL + [_i, _i, _i, _i, _i, _p, _i, _i, _p, _p, _p, _p, _i,
                                             _p, _z, _p, _p]),
-    "cmr_kv8_free": (ctypes.c_int, [_p, _i, _i, _p, _i, _p, _i, _p, _z, _p, _p]),
+    "cmr_kv8_free": (ctypes.c_int, [_p, _i, _i, _p, _i, _p, _i, _p, _p]),
     "cmr_kv8_compact": (ctypes.c_int, _POOL + [_i, _i, _i, _i, _i, _p, _i, _i, _p, _p, _z, _p,
                                                _p]),
     "cmr_kv8_pages_workspace_bytes": (_z, [_i, _i, _i]),
@@ -80,12 +80,13 @@ def lib() -> ctypes.CDLL:
     return _lib
 
 
-def _check(status: int, where: str):
-    if status != CMR_OK:
-        raise Kv8Error(status, where)
+def _raw_stream(dev: torch.device, stream: Optional[torch.cuda.Stream]) -> int:
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(dev.index)
 
 
-def _want(t, name: str, dtype: torch.dtype, dev: Optional[torch.device], shape=None):
+def _want(t, name: str, dtype: torch.dtype, dev: Optional[torch.device], shape=None) -> int:
     """t's data pointer, after the checks (shape: a tuple, None for any size in a place)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -103,17 +104,32 @@ def _want(t, name: str, dtype: torch.dtype, dev: Optional[torch.device], shape=N
     return t.data_ptr()
 
 
-def _maybe(t, name, dtype, dev, shape=None):
-    return None if t is None else _want(t, name, dtype, dev, shape)
+def _ptr(t, name: str, dtype: torch.dtype, dev: torch.device, shape: Tuple[int, ...]) -> int:
+    """_want for a known shape: the checks of a decode step's dozen tensors cost as
+    much host time as its launch, so the good case is told by four comparisons."""
+    if isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == shape and \
+            t.get_device() == dev.index and t.is_contiguous():
+        return t.data_ptr()
+    return _want(t, name, dtype, dev, shape)
+
+
+def _maybe(t, name, dtype, dev, shape):
+    return None if t is None else _ptr(t, name, dtype, dev, shape)
+
+
+def _status(t, dev):
+    return None if t is None else _want(t, "device_status", torch.int32, dev)
 
 
 def _pool(k_pages, v_pages, k_scales, v_scales, dev):
     """Pointers of the pool, and (L, pages, hk, P, D)."""
-    kp = _want(k_pages, "k_pages", torch.float8_e4m3fn, dev, (None,) * 5)
-    shape = tuple(k_pages.shape)
-    return (kp, _want(v_pages, "v_pages", torch.float8_e4m3fn, dev, shape),
-            _want(k_scales, "k_scales", torch.float32, dev, shape[:3]),
-            _want(v_scales, "v_scales", torch.float32, dev, shape[:3])), shape
+    kp = _want(k_pages, "k_pages", torch.float8_e4m3fn, dev)
+    shape = k_pages.shape
+    if len(shape) != 5:
+        raise ValueError(f"k_pages must be [L, pages, hk, P, D], got {list(shape)}")
+    return (kp, _ptr(v_pages, "v_pages", torch.float8_e4m3fn, dev, shape),
+            _ptr(k_scales, "k_scales", torch.float32, dev, shape[:3]),
+            _ptr(v_scales, "v_scales", torch.float32, dev, shape[:3])), shape
 
 
 def _heads(t, name, dev, n=None, L=None, D=None):
@@ -129,28 +145,53 @@ def _heads(t, name, dev, n=None, L=None, D=None):
     return p, s
 
 
-def _batch(cu_seqlens, pos_offset, slot, n, seqs, dev):
+def _table(page_table, dev):
+    """(pointer, rows, columns) of page_table."""
+    p = _want(page_table, "page_table", torch.int32, dev)
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [rows, max_pages]")
+    rows, cols = page_table.shape
+    return p, rows, cols
+
+
+def _batch(cu_seqlens, pos_offset, slot, n, dev):
     """(num_seqs, pointers of cu_seqlens, pos_offset and slot)."""
     if cu_seqlens is None:
-        b = n
+        b, cu = n, None
     else:
+        cu = _want(cu_seqlens, "cu_seqlens", torch.int32, dev)
         b = cu_seqlens.numel() - 1
-        if b < 0:
+        if b < 0 or cu_seqlens.dim() != 1:
             raise ValueError("cu_seqlens needs num_seqs + 1 entries")
-    if seqs is not None and seqs != b:
-        raise ValueError(f"start and amount hold {seqs} sequences, the batch {b}")
-    return b, _maybe(cu_seqlens, "cu_seqlens", torch.int32, dev, (b + 1,)), \
-        _maybe(pos_offset, "pos_offset", torch.int32, dev, (b,)), \
+    return b, cu, _maybe(pos_offset, "pos_offset", torch.int32, dev, (b,)), \
         _maybe(slot, "slot", torch.int32, dev, (b,))
 
 
-def _workspace(workspace, need, dev):
-    """(tensor, pointer, bytes): the caller's, or a new one."""
+def _workspace(workspace, need, dev, stream):
+    """(tensor, pointer, bytes): the caller's, or a new one that belongs to the stream
+    that runs the call."""
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
-    elif not workspace.is_cuda or workspace.device != dev or not workspace.is_contiguous():
+        if stream is None:
+            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+        else:
+            with torch.cuda.stream(stream):
+                workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+        return workspace, workspace.data_ptr(), max(need, 16)
+    if not workspace.is_cuda or workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous CUDA tensor on {dev}")
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _call(name: str, dev: torch.device, args):
+    """The C function, with dev as the current device."""
+    f = getattr(_lib or lib(), name)
+    if torch.cuda.current_device() == dev.index:
+        status = f(*args)
+    else:
+        with torch.cuda.device(dev):
+            status = f(*args)
+    if status != CMR_OK:
+        raise Kv8Error(status, name)
 
 
 def rotate_qk_kv8(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor,
@@ -166,11 +207,10 @@ def rotate_qk_kv8(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor,
     into the paged 8-bit cache.  cu_seqlens=None means one token per sequence (a
     decode step); slot gives each sequence's row of page_table (default: its
     own number).  Returns q."""
-    kp, (L, n, hk, D) = _heads(k, "k", None)
+    kp, shape = _heads(k, "k", None)
+    L, n, hk, D = shape
     dev = k.device
-    vp = _heads(v, "v", dev)
-    if vp[1] != (L, n, hk, D):
-        raise ValueError("v must have the shape of k")
+    vp = _ptr(v, "v", torch.bfloat16, dev, k.shape)
     qp, hq = None, 0
     if q is not None:
         qp, qs = _heads(q, "q", dev, n, L, D)
@@ -178,28 +218,27 @@ def rotate_qk_kv8(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor,
     pool, (pl, pages, phk, P, pd) = _pool(k_pages, v_pages, k_scales, v_scales, dev)
     if (pl, phk, pd) != (L, hk, D):
         raise ValueError(f"k_pages must be [L, pages, hk, P, D] = [{L}, pages, {hk}, P, {D}]")
-    table = _want(page_table, "page_table", torch.int32, dev, (None, None))
-    b, cu, off, sl = _batch(cu_seqlens, pos_offset, slot, n, start.numel(), dev)
-    sp = _want(start, "start", torch.int32, dev, (b,))
-    ap = _want(amount, "amount", torch.int32, dev, (b,))
-    st = _maybe(device_status, "device_status", torch.int32, dev)
-    sec = (_i * 3)(*[int(x) for x in sections])
-    if n == 0 or L == 0:
-        return q
-    with torch.cuda.device(dev):
-        _check(lib().cmr_kv8_rotate_qk(
-            qp if hq else None, kp, vp[0], cu, b, off, sp, ap, n, L, hq, hk, D, float(theta), sec,
-            int(rot_dim), *pool, pages, P, table, page_table.shape[0], page_table.shape[1], sl, st,
-            _stream_ptr(dev, stream)), "cmr_kv8_rotate_qk")
+    table, rows, cols = _table(page_table, dev)
+    b, cu, off, sl = _batch(cu_seqlens, pos_offset, slot, n, dev)
+    sp = _ptr(start, "start", torch.int32, dev, (b,))
+    ap = _ptr(amount, "amount", torch.int32, dev, (b,))
+    st = _status(device_status, dev)
+    if n and L:
+        _call("cmr_kv8_rotate_qk", dev, (
+            qp if hq else None, kp, vp, cu, b, off, sp, ap, n, L, hq, hk, D, theta,
+            (_i * 3)(*sections), rot_dim, *pool, pages, P, table, rows, cols, sl, st,
+            _raw_stream(dev, stream)))
     return q
 
 
 def attend_kv8_workspace_bytes(num_seqs: int, n_tokens: int, num_layers: int, hq: int, hk: int,
-                               head_dim: int) -> int:
-    """Workspace bytes of attend_kv8 for these sizes on the current device."""
-    return int(lib().cmr_kv8_attend_workspace_bytes(int(num_seqs), int(n_tokens),
-                                                    int(num_layers), int(hq), int(hk),
-                                                    int(head_dim)))
+                               head_dim: int, device: Optional[torch.device] = None) -> int:
+    """Workspace bytes of attend_kv8 for these sizes on a device (default: the current)."""
+    f = lib().cmr_kv8_attend_workspace_bytes
+    if device is None or device.index in (None, torch.cuda.current_device()):
+        return f(num_seqs, n_tokens, num_layers, hq, hk, head_dim)
+    with torch.cuda.device(device):
+        return f(num_seqs, n_tokens, num_layers, hq, hk, head_dim)
 
 
 def attend_kv8(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
@@ -219,23 +258,22 @@ def attend_kv8(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
     pool, (pl, pages, hk, P, pd) = _pool(k_pages, v_pages, k_scales, v_scales, dev)
     if (pl, pd) != (L, D):
         raise ValueError(f"k_pages must be [L, pages, hk, P, D] = [{L}, pages, hk, P, {D}]")
-    table = _want(page_table, "page_table", torch.int32, dev, (None, None))
-    b, cu, off, sl = _batch(cu_seqlens, pos_offset, slot, n, None, dev)
+    table, rows, cols = _table(page_table, dev)
+    b, cu, off, sl = _batch(cu_seqlens, pos_offset, slot, n, dev)
     if out is None:
-        out = torch.empty_like(q)
-    op = _want(out, "out", torch.bfloat16, dev, tuple(q.shape))
-    st = _maybe(device_status, "device_status", torch.int32, dev)
-    if n == 0 or L == 0:
-        return out
-    with torch.cuda.device(dev):
-        # a new workspace belongs to the stream that runs the call
-        with torch.cuda.stream(stream):
-            ws, wp, wb = _workspace(workspace, lib().cmr_kv8_attend_workspace_bytes(
-                b, n, L, hq, hk, D), dev)
-        _check(lib().cmr_kv8_attend(
-            qp, op, cu, b, off, n, L, hq, hk, D, D ** -0.5 if scale is None else float(scale),
-            *pool, pages, P, table, page_table.shape[0], page_table.shape[1], sl, wp, wb, st,
-            _stream_ptr(dev, stream)), "cmr_kv8_attend")
+        if stream is None:
+            out = torch.empty_like(q)
+        else:
+            with torch.cuda.stream(stream):
+                out = torch.empty_like(q)
+    op = _ptr(out, "out", torch.bfloat16, dev, q.shape)
+    st = _status(device_status, dev)
+    if n and L:
+        ws, wp, wb = _workspace(workspace, attend_kv8_workspace_bytes(b, n, L, hq, hk, D, dev)
+                                if workspace is None else 0, dev, stream)
+        _call("cmr_kv8_attend", dev, (
+            qp, op, cu, b, off, n, L, hq, hk, D, D ** -0.5 if scale is None else scale, *pool,
+            pages, P, table, rows, cols, sl, wp, wb, st, _raw_stream(dev, stream)))
     return out
 
 
@@ -249,20 +287,19 @@ def kv8_pages_workspace_bytes(table_rows: int, num_pages: int, n: int = 0) -> in
     return int(lib().cmr_kv8_pages_workspace_bytes(int(table_rows), int(num_pages), int(n)))
 
 
-def _pages_state(page_table, page_refs):
-    t = _want(page_table, "page_table", torch.int32, None, (None, None))
-    return t, _want(page_refs, "page_refs", torch.int32, page_table.device, (None,)), \
-        page_table.device
+def _pages_state(page_table, page_refs, pages=None):
+    """(device, pointer of the table, rows, columns, pointer of the counts, pages)."""
+    t, rows, cols = _table(page_table, None)
+    dev = page_table.device
+    r = _want(page_refs, "page_refs", torch.int32, dev, (pages,))
+    return dev, t, rows, cols, r, page_refs.shape[0]
 
 
 def _pages_call(name, dev, before, after, rows, pages, n, workspace, device_status, stream):
-    st = _maybe(device_status, "device_status", torch.int32, dev)
-    l = lib()
-    with torch.cuda.device(dev):
-        with torch.cuda.stream(stream):
-            ws, wp, wb = _workspace(workspace, l.cmr_kv8_pages_workspace_bytes(rows, pages, n),
-                                    dev)
-        _check(getattr(l, name)(*before, *after, wp, wb, st, _stream_ptr(dev, stream)), name)
+    st = _status(device_status, dev)
+    ws, wp, wb = _workspace(workspace, kv8_pages_workspace_bytes(rows, pages, n)
+                            if workspace is None else 0, dev, stream)
+    _call(name, dev, (*before, *after, wp, wb, st, _raw_stream(dev, stream)))
 
 
 def kv8_extend(page_table: torch.Tensor, page_refs: torch.Tensor, slots: torch.Tensor,
@@ -271,15 +308,13 @@ def kv8_extend(page_table: torch.Tensor, page_refs: torch.Tensor, slots: torch.T
                stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """cmr_kv8_extend: give rows slots the pages that they lack to hold lens tokens.
     Returns page_table."""
-    t, r, dev = _pages_state(page_table, page_refs)
+    dev, t, rows, cols, r, pages = _pages_state(page_table, page_refs)
     n = slots.numel()
-    s = _want(slots, "slots", torch.int32, dev, (n,))
-    ln = _want(lens, "lens", torch.int32, dev, (n,))
+    s = _ptr(slots, "slots", torch.int32, dev, (n,))
+    ln = _ptr(lens, "lens", torch.int32, dev, (n,))
     if n:
-        rows, cols = page_table.shape
-        _pages_call("cmr_kv8_extend", dev, (t, rows, cols, r, page_refs.numel(),
-                                            int(page_tokens)), (s, ln, n), rows,
-                    page_refs.numel(), n, workspace, device_status, stream)
+        _pages_call("cmr_kv8_extend", dev, (t, rows, cols, r, pages, page_tokens), (s, ln, n),
+                    rows, pages, n, workspace, device_status, stream)
     return page_table
 
 
@@ -291,34 +326,30 @@ def kv8_fork(k_pages: torch.Tensor, v_pages: torch.Tensor, k_scales: torch.Tenso
              stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """cmr_kv8_fork: make the empty rows dst hold the first lens tokens of rows src,
     whole pages shared and the rest copied.  Returns page_table."""
-    t, r, dev = _pages_state(page_table, page_refs)
+    dev = page_table.device
     pool, (L, pages, hk, P, D) = _pool(k_pages, v_pages, k_scales, v_scales, dev)
-    if pages != page_refs.numel():
-        raise ValueError(f"page_refs counts {page_refs.numel()} pages, the pool holds {pages}")
+    dev, t, rows, cols, r, pages = _pages_state(page_table, page_refs, pages)
     n = src.numel()
-    s = _want(src, "src", torch.int32, dev, (n,))
-    d = _want(dst, "dst", torch.int32, dev, (n,))
-    ln = _want(lens, "lens", torch.int32, dev, (n,))
+    s = _ptr(src, "src", torch.int32, dev, (n,))
+    d = _ptr(dst, "dst", torch.int32, dev, (n,))
+    ln = _ptr(lens, "lens", torch.int32, dev, (n,))
     if n:
-        rows, cols = page_table.shape
         _pages_call("cmr_kv8_fork", dev, pool + (L, hk, D, pages, P, t, rows, cols, r),
                     (s, d, ln, n), rows, pages, n, workspace, device_status, stream)
     return page_table
 
 
 def kv8_free(page_table: torch.Tensor, page_refs: torch.Tensor, slots: torch.Tensor,
-             workspace: Optional[torch.Tensor] = None,
              device_status: Optional[torch.Tensor] = None,
              stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """cmr_kv8_free: empty rows slots, one holder less for each of their pages.
     Returns page_table."""
-    t, r, dev = _pages_state(page_table, page_refs)
+    dev, t, rows, cols, r, pages = _pages_state(page_table, page_refs)
     n = slots.numel()
-    s = _want(slots, "slots", torch.int32, dev, (n,))
+    s = _ptr(slots, "slots", torch.int32, dev, (n,))
     if n:
-        rows, cols = page_table.shape
-        _pages_call("cmr_kv8_free", dev, (t, rows, cols, r, page_refs.numel()), (s, n), rows,
-                    page_refs.numel(), n, workspace, device_status, stream)
+        _call("cmr_kv8_free", dev, (t, rows, cols, r, pages, s, n, _status(device_status, dev),
+                                    _raw_stream(dev, stream)))
     return page_table
 
 
@@ -329,11 +360,10 @@ def kv8_compact(k_pages: torch.Tensor, v_pages: torch.Tensor, k_scales: torch.Te
                 stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """cmr_kv8_compact: move pages so that those in use are the pool's first.
     Returns page_table."""
-    t, r, dev = _pages_state(page_table, page_refs)
+    dev = page_table.device
     pool, (L, pages, hk, P, D) = _pool(k_pages, v_pages, k_scales, v_scales, dev)
-    if pages != page_refs.numel():
-        raise ValueError(f"page_refs counts {page_refs.numel()} pages, the pool holds {pages}")
-    rows, cols = page_table.shape
-    _pages_call("cmr_kv8_compact", dev, pool + (L, hk, D, pages, P, t, rows, cols, r), (), rows,
-                pages, 0, workspace, device_status, stream)
+    dev, t, rows, cols, r, pages = _pages_state(page_table, page_refs, pages)
+    if L:
+        _pages_call("cmr_kv8_compact", dev, pool + (L, hk, D, pages, P, t, rows, cols, r), (),
+                    rows, pages, 0, workspace, device_status, stream)
     return page_table
