@@ -19,6 +19,10 @@ size_t attend_tiles_workspace(int32_t num_seqs, int64_t n_tokens, int32_t num_la
                               int32_t hk, int32_t head_dim);
 cudaError_t launch_attend_tiles(const AttendArgs& a, cudaStream_t stream, bool* launched);
 
+// Tensor maps of the pool's codes, [unit = (layer, page, head)][row of the page][dim],
+// for boxes of `rows` rows of up to 128 dims, swizzled by as many bytes.
+bool encode_pool_maps(const Pool& pool, uint32_t rows, CUtensorMap* k, CUtensorMap* v);
+
 // Item slots per (layer, KV head) that the tokens of a call can need.
 inline int64_t item_slots(int32_t num_seqs, int64_t n_tokens, int group, int R, bool step) {
   return step ? static_cast<int64_t>(num_seqs) * ((group + R - 1) / R)
@@ -26,6 +30,21 @@ inline int64_t item_slots(int32_t num_seqs, int64_t n_tokens, int group, int R, 
 }
 
 #ifdef __CUDACC__
+
+// Byte offset of 16-byte chunk c of row r in a panel.
+template <int W>
+__device__ __forceinline__ int swizzled(int r, int c) {
+  return W == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+}
+
+__device__ __forceinline__ void load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x,
+                                        int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
 
 struct Item {
   int32_t b, row;      // sequence and its table row (-1: none)

@@ -57,6 +57,8 @@ template <int D, int NQ>
 struct Smem {
   static constexpr int R = 8 * NQ;
   static constexpr int kStages = NQ == 1 ? 3 : 2;
+  static constexpr int W = D < 128 ? D : 128;                      // bytes of a swizzled row
+  static constexpr int kPanel = kTile * W;                         // W dims of a tile
   static constexpr int kStage = 2 * kTile * D;
   static constexpr int kQ = kStages * kStage;                      // f16 fragments of Q
   static constexpr int kNan = kQ + (D / 16) * NQ * 32 * 8;         // [2][D] ints
@@ -103,27 +105,30 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return r;
 }
 
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
-                                          uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-          dst),
-      "l"(src), "r"(bytes), "r"(bar)
-      : "memory");
-}
+// The token of a warp's 16 that row m < 8 of S^T stands for (m + 8: 8 further).  Any
+// order will do, as long as P^T and V^T follow it; with this one, and rows swizzled
+// as TMA leaves them, the eight lanes that read shared memory together hit different
+// banks, both for keys (lanes of rows m, m + 1) and for values (even or odd m).
+__device__ __forceinline__ int token_of(int m) { return m ^ ((m & 1) << 2); }
 
 // Work is counted in tiles, and kLead more for each item: what it costs to start
 // and to finish one.  Places [start, start + kLead) of an item's stretch hold no
-// tile.
-constexpr int kLead = 2;
+// tile.  128 sequences of 1 to 7,698 tokens: 54 us without, 33 with 2, 26.6 with 4,
+// 28 with 6; 64 of 4,096: 54.7, 54.6, 53.2, 52.6.
+constexpr int kLead = 4;
 
 template <int D, int NQ>
-__global__ void __launch_bounds__(kThreads, NQ == 1 ? 2 : 1) attend_rows_kernel(const RowsArgs ra) {
+__global__ void __launch_bounds__(kThreads, NQ == 1 ? 2 : 1)
+    attend_rows_kernel(const RowsArgs ra, const __grid_constant__ CUtensorMap k_map,
+                       const __grid_constant__ CUtensorMap v_map) {
   using S = Smem<D, NQ>;
   constexpr int R = S::R;
   constexpr int NS = S::kStages;
   constexpr int M = D / 16;  // O^T's row blocks
-  extern __shared__ __align__(128) uint8_t smem[];
+  constexpr int W = S::W;
+  constexpr int kPanels = D / W;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024 - (tma::smem_addr(smem_raw) & 1023)) & 1023);
   const AttendArgs& a = ra.a;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid & 31;
   uint2* s_q = reinterpret_cast<uint2*>(smem + S::kQ);
@@ -212,17 +217,15 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? 2 : 1) attend_rows_kernel(
     // ---- producer: lane 4 i + g looks after tokens [16g, 16g + 16) of place i of a
     // batch of eight
     const int g = lane & 3;
-    const int span = min(P, kTile);
     uint32_t problems = 0;
     struct Look {
       bool tile;      // the place holds a tile
       int64_t unit;   // its page's (layer, page, head), or -1
-      int rows;       // rows that this lane copies
       int64_t tok;
       float ks, vs;
     };
     auto look = [&](int64_t w0) {
-      Look k{false, -1, 0, 0, 0.f, 1.f};
+      Look k{false, -1, 0, 0.f, 1.f};
       const int64_t w = w0 + (lane >> 2);
       if (w >= run_hi) return k;
       const int64_t lh = w / max(total, 1);
@@ -244,10 +247,6 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? 2 : 1) attend_rows_kernel(
       k.unit = (static_cast<int64_t>(l) * a.pool.num_pages + id) * a.pool.hk + h;
       k.ks = __ldg(a.pool.ks + k.unit);
       k.vs = __ldg(a.pool.vs + k.unit);
-      // the lane that copies for a page (or for 64 tokens of a larger one) takes
-      // the rows up to the last one seen, in whole groups of 16
-      if ((16 * g) % span == 0)
-        k.rows = static_cast<int>(min(static_cast<int64_t>(span), (seen - k.tok + 15) / 16 * 16));
       return k;
     };
     int stage = 0, phase = 0, issued = 0;
@@ -255,22 +254,26 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? 2 : 1) attend_rows_kernel(
     Look now = look(run_lo);
     for (int64_t w = run_lo; w < run_hi && !dead; w += 8) {
       const uint32_t tiles = __ballot_sync(~0u, now.tile);
-      int bytes = now.rows + __shfl_xor_sync(~0u, now.rows, 1);
-      bytes = (bytes + __shfl_xor_sync(~0u, bytes, 2)) * 2 * D;
+      const uint32_t pages = __ballot_sync(~0u, now.unit >= 0);
       for (int i = 0; i < 8; ++i) {
         if (!((tiles >> (4 * i)) & 1u)) continue;
         if (issued >= NS && !tma::mbar_wait(empty0 + 8 * stage, phase ^ 1)) dead = true;
         dead = __any_sync(~0u, dead);
         if (dead) break;
         const uint32_t bar = full0 + 8 * stage;
-        if (lane == 4 * i) tma::mbar_arrive_expect_tx(bar, bytes);
+        if (lane == 4 * i)
+          tma::mbar_arrive_expect_tx(bar, __popc((pages >> (4 * i)) & 15u) * 2 * 16 * D);
         __syncwarp();
         const bool mine = (lane >> 2) == i;
-        if (mine && now.rows > 0) {
-          const int64_t src = now.unit * (static_cast<int64_t>(P) * D) + (now.tok & (P - 1)) * D;
-          const uint32_t dst = stage0 + stage * S::kStage + 16 * g * D;
-          bulk_load(dst, a.pool.k + src, now.rows * D, bar);
-          bulk_load(dst + kTile * D, a.pool.v + src, now.rows * D, bar);
+        if (mine && now.unit >= 0) {
+          const uint32_t dst = stage0 + stage * S::kStage + 16 * g * W;
+          const int row = static_cast<int>(now.tok) & (P - 1), unit = static_cast<int>(now.unit);
+#pragma unroll
+          for (int x = 0; x < kPanels; ++x)
+            load_3d(dst + x * S::kPanel, &k_map, bar, x * W, row, unit);
+#pragma unroll
+          for (int x = 0; x < kPanels; ++x)
+            load_3d(dst + kTile * D + x * S::kPanel, &v_map, bar, x * W, row, unit);
         }
         // the scales, under the copies
         const bool good = now.unit >= 0 && scale_ok(now.ks) && scale_ok(now.vs);
@@ -457,8 +460,6 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? 2 : 1) attend_rows_kernel(
     for (int tile = 0; tile < sg.nt; ++tile) {
       if (!dead && !tma::mbar_wait(full0 + 8 * stage, phase, tma::kConsumerWaitLimitNs)) dead = true;
       used = smem + stage * S::kStage;
-      const uint8_t* kt = used + warp * 16 * D;
-      const uint8_t* vt = kt + kTile * D;
       const StageInfo& info = s_info[stage];
       const float k_scale = info.k_scale[warp], v_log2 = info.v_log2[warp];
       const float v_inv = info.v_inv[warp];
@@ -466,19 +467,22 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? 2 : 1) attend_rows_kernel(
       const bool live = ((info.valid >> warp) & 1u) && tok0 < vis_last;
 
       if (live) {
-        // scores of tokens tok0 + g and + g + 8 against queries 2t, 2t + 1, summed
-        // over the dims in four chains
-        float part[4][NQ][4];
+        // scores of two tokens against queries 2t, 2t + 1, summed over the dims in
+        // two chains
+        float part[2][NQ][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
           for (int n = 0; n < NQ; ++n)
 #pragma unroll
             for (int x = 0; x < 4; ++x) part[i][n][x] = 0.f;
 #pragma unroll
         for (int j = 0; j < D / 64; ++j) {
-          const uint4 lo = *reinterpret_cast<const uint4*>(kt + g * D + j * 64 + t * 16);
-          const uint4 hi = *reinterpret_cast<const uint4*>(kt + (g + 8) * D + j * 64 + t * 16);
+          const int r = warp * 16 + token_of(g);
+          const int c = j * 4 + t;  // 16-byte chunk of the keys
+          const uint8_t* src = used + c / (W / 16) * S::kPanel;
+          const uint4 lo = *reinterpret_cast<const uint4*>(src + swizzled<W>(r, c % (W / 16)));
+          const uint4 hi = *reinterpret_cast<const uint4*>(src + swizzled<W>(r + 8, c % (W / 16)));
           const uint32_t wl[4] = {lo.x, lo.y, lo.z, lo.w}, wh[4] = {hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -487,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? 2 : 1) attend_rows_kernel(
 #pragma unroll
             for (int n = 0; n < NQ; ++n) {
               const uint2 q = s_q[((j * 4 + i) * NQ + n) * 32 + lane];
-              mma_f16(part[i][n], a0, a1, a2, a3, q.x, q.y);
+              mma_f16(part[i & 1][n], a0, a1, a2, a3, q.x, q.y);
             }
           }
         }
@@ -499,8 +503,8 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? 2 : 1) attend_rows_kernel(
         for (int n = 0; n < NQ; ++n) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int tok = tok0 + g + (i >= 2 ? 8 : 0);
-            const float dot = (part[0][n][i] + part[1][n][i]) + (part[2][n][i] + part[3][n][i]);
+            const int tok = tok0 + token_of(g) + (i >= 2 ? 8 : 0);
+            const float dot = part[0][n][i] + part[1][n][i];
             const float x = fmaf(dot, mult[n][i & 1] * k_scale, v_log2);
             s[n][i] = tok < vis[n][i & 1] ? x : -INFINITY;
           }
@@ -554,16 +558,17 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? 2 : 1) attend_rows_kernel(
           uint32_t v[4][VW];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int tk = 2 * t + (i & 1) + (i >= 2 ? 8 : 0);
-            const uint8_t* src = vt + tk * D + hh * 32 * VW + g * 4 * VW;
+            const int r = warp * 16 + token_of(2 * t + (i & 1)) + (i >= 2 ? 8 : 0);
+            const uint8_t* src = used + kTile * D + hh * S::kPanel;
             if constexpr (VW == 4) {
-              const uint4 x = *reinterpret_cast<const uint4*>(src);
+              const uint4 x = *reinterpret_cast<const uint4*>(src + swizzled<W>(r, g));
               v[i][0] = x.x;
               v[i][1] = x.y;
               v[i][2] = x.z;
               v[i][3] = x.w;
             } else {
-              const uint2 x = *reinterpret_cast<const uint2*>(src);
+              const uint2 x =
+                  *reinterpret_cast<const uint2*>(src + swizzled<W>(r, g / 2) + (g & 1) * 8);
               v[i][0] = x.x;
               v[i][1] = x.y;
             }
@@ -574,7 +579,7 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? 2 : 1) attend_rows_kernel(
             // given back, at the end, to the rows that see it.
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const int tok = tok0 + 2 * t + (i & 1) + (i >= 2 ? 8 : 0);
+              const int tok = tok0 + token_of(2 * t + (i & 1)) + (i >= 2 ? 8 : 0);
 #pragma unroll
               for (int x = 0; x < VW; ++x) {
                 if (tok >= vis_last) {
@@ -945,21 +950,22 @@ int max_ctas(int R) {
 size_t align16(size_t x) { return (x + 15) / 16 * 16; }
 
 template <int D, int NQ>
-cudaError_t launch(RowsArgs ra, cudaStream_t stream) {
+cudaError_t launch(const RowsArgs& ra, const CUtensorMap& k, const CUtensorMap& v,
+                   cudaStream_t stream) {
   using S = Smem<D, NQ>;
   const AttendArgs& a = ra.a;
   const int64_t lh = static_cast<int64_t>(a.pool.num_layers) * a.pool.hk;
-  const size_t smem = S::kItems + (3 * (ra.ctas > 0 ? ra.items : 1) + 1) * sizeof(int);
+  const size_t smem = 1024 + S::kItems + (3 * (ra.ctas > 0 ? ra.items : 1) + 1) * sizeof(int);
   cudaError_t e = cudaFuncSetAttribute(
       attend_rows_kernel<D, NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-      static_cast<int>(S::kItems + (3 * kMaxSplitItems + 1) * sizeof(int)));
+      static_cast<int>(1024 + S::kItems + (3 * kMaxSplitItems + 1) * sizeof(int)));
   if (e != cudaSuccess) return e;
   if (ra.ctas == 0) {
     if (lh > 65535) return cudaErrorInvalidValue;
-    attend_rows_kernel<D, NQ><<<dim3(ra.items, static_cast<unsigned>(lh)), kThreads, smem, stream>>>(ra);
+    attend_rows_kernel<D, NQ><<<dim3(ra.items, static_cast<unsigned>(lh)), kThreads, smem, stream>>>(ra, k, v);
     return cudaGetLastError();
   }
-  attend_rows_kernel<D, NQ><<<ra.ctas, kThreads, smem, stream>>>(ra);
+  attend_rows_kernel<D, NQ><<<ra.ctas, kThreads, smem, stream>>>(ra, k, v);
   e = cudaGetLastError();
   if (e != cudaSuccess || ra.ctas == 1) return e;
   // With one item to four runs or more, an item is cut into a few pieces: a CTA
@@ -1015,11 +1021,26 @@ cudaError_t launch_attend_rows(const AttendArgs& a, cudaStream_t stream) {
     // the joining grid has a block for every item and row
     if (nb * a.pool.num_layers * a.pool.hk > INT32_MAX) return cudaErrorInvalidValue;
   }
+  CUtensorMap k, v;
+  if (!encode_pool_maps(a.pool, 16, &k, &v)) return cudaErrorNotSupported;
   switch (a.pool.head_dim) {
-    case 64: return R == 8 ? launch<64, 1>(ra, stream) : launch<64, 2>(ra, stream);
-    case 128: return R == 8 ? launch<128, 1>(ra, stream) : launch<128, 2>(ra, stream);
-    default: return R == 8 ? launch<256, 1>(ra, stream) : launch<256, 2>(ra, stream);
+    case 64: return R == 8 ? launch<64, 1>(ra, k, v, stream) : launch<64, 2>(ra, k, v, stream);
+    case 128: return R == 8 ? launch<128, 1>(ra, k, v, stream) : launch<128, 2>(ra, k, v, stream);
+    default: return R == 8 ? launch<256, 1>(ra, k, v, stream) : launch<256, 2>(ra, k, v, stream);
   }
+}
+
+bool encode_pool_maps(const Pool& pool, uint32_t rows, CUtensorMap* k, CUtensorMap* v) {
+  const int64_t units = static_cast<int64_t>(pool.num_layers) * pool.hk * pool.num_pages;
+  if (units > INT32_MAX) return false;
+  const uint32_t P = 1u << pool.page_shift;
+  const uint32_t W = pool.head_dim < 128 ? pool.head_dim : 128;
+  const uint64_t D = static_cast<uint64_t>(pool.head_dim);
+  const uint64_t dims[3] = {D, P, static_cast<uint64_t>(units)};
+  const uint64_t strides[2] = {D, D * P};
+  const uint32_t box[3] = {W, rows, 1};
+  return encode_u8_tensor_map(k, pool.k, 3, dims, strides, box, static_cast<int>(W)) &&
+         encode_u8_tensor_map(v, pool.v, 3, dims, strides, box, static_cast<int>(W));
 }
 
 cudaError_t launch_attend(const AttendArgs& a, cudaStream_t stream) {

@@ -85,21 +85,6 @@ struct TilesArgs {
   float* partial;  // [layers x heads x items][splits][128][D], then the rows' ref and sum
 };
 
-// Byte offset of 16-byte chunk c of row r in a panel.
-template <int W>
-__device__ __forceinline__ int swizzled(int r, int c) {
-  return W == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
-}
-
-__device__ __forceinline__ void load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x,
-                                        int y, int z) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
-      "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z)
-      : "memory");
-}
-
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -347,8 +332,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // s = 2^e with max |q| in (224 s, 448 s]
       int e = static_cast<int>(mx >> 7) - 127 - 8 + ((mx & 0x7fu) > 0x60u ? 1 : 0);
       e = mx == 0 ? 0 : max(-126, e);
-      const float inv = __int_as_float((127 - e) << 23);
-      mult = mx < 0x7f80u ? a.scale_log2 * __int_as_float((127 + e) << 23)
+      // a negative softmax scale turns q around, so that scores only grow with S
+      const float inv = copysignf(__int_as_float((127 - e) << 23), a.scale_log2);
+      mult = mx < 0x7f80u ? fabsf(a.scale_log2) * __int_as_float((127 + e) << 23)
                           : __int_as_float(0x7fffffff);  // the row becomes NaN
 #pragma unroll
       for (int c = 0; c < kChunks; c += 2) {
@@ -397,45 +383,60 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::ld32(x[1], tmem_s[i & 1] + lanes + 64 * half + 32);
       tc::wait_ld();
 
+      // the exponent of a weight is S f + c, with f and c of the token's page
+      float f[4], c[4];
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        f[g] = mult * info.k_scale[4 * half + g];
+        c[g] = info.v_log2[4 * half + g];
+      }
+      if (edge) {
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const int tok = tile + 64 * half + 16 * g + j;
+            const float y = fmaf(__uint_as_float(x[g / 2][g % 2 * 16 + j]), f[g], c[g]);
+            x[g / 2][g % 2 * 16 + j] = __float_as_uint(
+                tok < seen && ((valid >> (4 * half + g)) & 1u) ? y : -INFINITY);
+          }
+          f[g] = 1.f;
+          c[g] = 0.f;
+        }
+      }
       float mx = -INFINITY;
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
-        const float f = mult * info.k_scale[4 * half + g], add = info.v_log2[4 * half + g];
+        float top = __uint_as_float(x[g / 2][g % 2 * 16]);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          float y = fmaf(__uint_as_float(x[g / 2][g % 2 * 16 + j]), f, add);
-          if (edge) {
-            const int tok = tile + 64 * half + 16 * g + j;
-            y = tok < seen && ((valid >> (4 * half + g)) & 1u) ? y : -INFINITY;
-          }
-          x[g / 2][g % 2 * 16 + j] = __float_as_uint(y);
-          mx = fmaxf(mx, y);
-        }
+        for (int j = 1; j < 16; ++j) top = fmaxf(top, __uint_as_float(x[g / 2][g % 2 * 16 + j]));
+        mx = fmaxf(mx, fmaf(top, f[g], c[g]));
       }
-      // the row's maximum over both halves; every thread has read its part of S
+      // the row's maximum over both halves; the two warps of these rows have read
+      // their parts of S
       float* ex = s_max + (i & 1) * 2 * kRows;
       ex[half * kRows + row] = mx;
       tc::fence_before();
-      tma::named_sync(1, kSoftmax);
+      tma::named_sync(2 + (warp & 3), 64);
       tc::fence_after();
       mx = fmaxf(mx, ex[(1 - half) * kRows + row]);
       const bool move = mx > ref + kLazy;
       if (__any_sync(~0u, move)) {
         const float to = fmaxf(ref, mx);
-        const float f = to == -INFINITY ? 1.f : exp2_approx(ref - to);
+        const float down = to == -INFINITY ? 1.f : exp2_approx(ref - to);
         ref = to;
-        sum *= f;
+        sum *= down;
         if (i > 0) {
           wait(o_done, i - 1);
           tc::fence_after();
 #pragma unroll
-          for (int c = 0; c < D / 2; c += 32) {
+          for (int d = 0; d < D / 2; d += 32) {
             uint32_t o[32];
-            tc::ld32(o, tmem + lanes + half * (D / 2) + c);
+            tc::ld32(o, tmem + lanes + half * (D / 2) + d);
             tc::wait_ld();
 #pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-            tc::st32(tmem + lanes + half * (D / 2) + c, o);
+            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * down);
+            tc::st32(tmem + lanes + half * (D / 2) + d, o);
           }
         }
       }
@@ -444,14 +445,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t t1[16], t2[16], t3[16];
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
-        float part = 0.f;
+        const float less = c[g] - shift;
+        float part[2] = {0.f, 0.f};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {  // 4 tokens: a word of each term
           float p[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            p[k] = exp2_approx(__uint_as_float(x[g / 2][g % 2 * 16 + 4 * j + k]) - shift);
-            part += p[k];
+            p[k] = exp2_approx(fmaf(__uint_as_float(x[g / 2][g % 2 * 16 + 4 * j + k]), f[g], less));
+            part[k & 1] += p[k];
           }
           // rounded to 9 significant bits, then three times 3 of them
           const uint32_t a0 = (pack_f16x2(p[0], p[1]) + 0x00020002u) & 0xfffcfffcu;
@@ -462,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           t2[4 * g + j] = __byte_perm(b0, b1, 0x7531);
           t3[4 * g + j] = __byte_perm(c0, c1, 0x7531);
         }
-        sum = fmaf(part, info.v_inv[4 * half + g], sum);
+        sum = fmaf(part[0] + part[1], info.v_inv[4 * half + g], sum);
       }
       tc::st16(tmem_s[i & 1] + lanes + 16 * half, t1);
       tc::st16(tmem_s[i & 1] + lanes + 32 + 16 * half, t2);
@@ -652,27 +654,18 @@ cudaError_t launch_attend_tiles(const AttendArgs& a, cudaStream_t stream, bool* 
   *launched = false;
   const Pool& pool = a.pool;
   const int64_t lh = static_cast<int64_t>(pool.num_layers) * pool.hk;
-  const int64_t units = lh * pool.num_pages;
   const int64_t items = item_slots(a.batch.num_seqs, a.batch.n_tokens, a.group, kRows,
                                    a.batch.cu == nullptr);
-  if (lh > 65535 || units > INT32_MAX || items * lh > INT32_MAX) return cudaSuccess;
-  const int D = pool.head_dim;
-  const int W = D < 128 ? D : 128;
-  const uint32_t P = 1u << pool.page_shift;
-  const uint64_t dims[3] = {static_cast<uint64_t>(D), P, static_cast<uint64_t>(units)};
-  const uint64_t strides[2] = {static_cast<uint64_t>(D), static_cast<uint64_t>(D) * P};
-  const uint32_t box[3] = {static_cast<uint32_t>(W), P, 1};
+  if (lh > 65535 || items * lh > INT32_MAX) return cudaSuccess;
   CUtensorMap k, v;
-  if (!encode_u8_tensor_map(&k, pool.k, 3, dims, strides, box, W) ||
-      !encode_u8_tensor_map(&v, pool.v, 3, dims, strides, box, W))
-    return cudaSuccess;
+  if (!encode_pool_maps(pool, 1u << pool.page_shift, &k, &v)) return cudaSuccess;
   TilesArgs ta{};
   ta.a = a;
   ta.items = static_cast<int32_t>(items);
   ta.splits = splits_for(items * lh);
   ta.partial = static_cast<float*>(a.workspace);
   *launched = true;
-  switch (D) {
+  switch (pool.head_dim) {
     case 64: return launch<64>(ta, k, v, lh, stream);
     case 128: return launch<128>(ta, k, v, lh, stream);
     default: return launch<256>(ta, k, v, lh, stream);
