@@ -988,6 +988,7 @@ size_t attend_rows_workspace(int32_t num_seqs, int64_t n_tokens, int32_t hq, int
   size_t most = 0;
   const int group = hq / hk;
   for (const bool step : {false, true}) {
+    if (step && num_seqs != n_tokens) continue;
     const int R = rows_of(group, step);
     const int64_t nb = item_slots(num_seqs, n_tokens, group, R, step);
     if (nb > kMaxSplitItems) continue;

@@ -12,7 +12,7 @@
 //       2^-19 of it);
 //   p = p1 + p2 + p3, e5m2: e5m2 is the upper byte of f16, so with p rounded to 9
 //       significant bits in f16, p1 is its upper byte, p2 that of what is left,
-//       p3 that of the rest, exactly (down to 2^-27 of the row's largest weight).
+//       p3 that of the rest, exactly (down to 2^-25 of the row's largest weight).
 // p thus carries the rounding that bf16 weights would (2^-9), and S and O are fp32
 // accumulators in tensor memory.  The scales enter as in attend_rows.cu: keys' in
 // the exponent's factor, values' in the exponent, and 2^-e in the sum of weights.
@@ -22,10 +22,10 @@
 // to f16 in shared memory instead (2 x 128 steps' worth) would pay 96 KB of shared
 // memory traffic per tile, more than the third term costs.
 //
-// Warps: 0 loads, 1 issues the products, 4-11 do the softmax: two threads to a
-// row, 64 of a tile's tokens each.  S has two buffers, so QK of the next tile runs
+// Warps: 0 loads, 1 issues the products, 2-3 clear values that must not be seen,
+// 4-11 do the softmax: two threads to a row, 64 of a tile's tokens each.  S has two buffers, so QK of the next tile runs
 // while this one's softmax does; p's terms take the place of S.  The reference of
-// the running softmax moves only when weights pass 2^4 times it, and O is scaled
+// the running softmax moves only when weights pass 2^6 times it, and O is scaled
 // again only then.
 #include "attend.cuh"
 #include "kv8.cuh"
@@ -47,11 +47,12 @@ constexpr int kTile = 128;     // tokens of a tile
 constexpr int kStages = 2;     // K and V tiles in flight
 constexpr int kInfos = 4;      // a tile's scales outlive its keys by the softmax
 constexpr int kSoftmax = 256;  // threads
+constexpr int kCleaners = 64;
 constexpr int kFirstWarp = 4;  // of the softmax
 constexpr int kThreads = kSoftmax + 32 * kFirstWarp;
 constexpr int kMaxSplits = 16;
-constexpr float kBase = 11.f;  // weights are at most 2^11 when the reference moves
-constexpr float kLazy = 4.f;   // and 2^15 before it does
+constexpr float kBase = 9.f;   // weights are at most 2^9 when the reference moves
+constexpr float kLazy = 6.f;   // and 2^15 before it does
 constexpr uint32_t kColumns = 512;
 
 struct TileInfo {
@@ -72,9 +73,10 @@ struct Smem {
   static constexpr int kNan = kV + kStages * kTileBytes;
   static constexpr int kMax = kNan + D * 4;             // [2][2][128] floats
   static constexpr int kSum = kMax + 4 * kRows * 4;     // [2][128]
-  static constexpr int kInfo = kSum + 2 * kRows * 4;
+  static constexpr int kAt = kSum + 2 * kRows * 4;      // [128] element offsets, 8 bytes
+  static constexpr int kInfo = kAt + kRows * 8;
   static constexpr int kBars = (kInfo + kInfos * static_cast<int>(sizeof(TileInfo)) + 7) / 8 * 8;
-  static constexpr int kMisc = kBars + 8 * (4 * kStages + 7);
+  static constexpr int kMisc = kBars + 8 * (5 * kStages + 7);
   static constexpr int kBytes = kMisc + 16 + 1024;  // and room to align
 };
 
@@ -96,6 +98,11 @@ __device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
+// The bytes of a word that are e4m3's NaN, as their upper bits.
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
+  return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+}
+
 // The split of an item's tiles: tiles of one CTA, and how many CTAs have any.
 __device__ __forceinline__ int split_tiles(int nt, int splits) { return (nt + splits - 1) / splits; }
 
@@ -113,9 +120,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   int* s_nan = reinterpret_cast<int*>(smem + S::kNan);
   float* s_max = reinterpret_cast<float*>(smem + S::kMax);
   float* s_sum = reinterpret_cast<float*>(smem + S::kSum);
+  int64_t* s_at = reinterpret_cast<int64_t*>(smem + S::kAt);  // of the query rows, in Q and out
   TileInfo* s_info = reinterpret_cast<TileInfo*>(smem + S::kInfo);
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + S::kMisc);
   volatile int* s_dead = reinterpret_cast<volatile int*>(s_tmem + 1);
+  volatile int* s_nan_taken = s_dead + 1;
   const uint32_t q_smem = tma::smem_addr(smem + S::kQ);
   const uint32_t k_smem = tma::smem_addr(smem + S::kK);
   const uint32_t v_smem = tma::smem_addr(smem + S::kV);
@@ -124,7 +133,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t v_full = bars + 16 * kStages, v_empty = bars + 24 * kStages;
   const uint32_t s_full = bars + 32 * kStages, p_full = s_full + 16;
   const uint32_t o_done = s_full + 32, q_ready = s_full + 40, drained = s_full + 48;
+  const uint32_t v_clean = s_full + 56;
 
+  if (warp == 1) tc::alloc(tma::smem_addr(s_tmem), kColumns);
   // ---- the item: heavy (late) row tiles first
   const int32_t bi = ta.items - 1 - static_cast<int32_t>(blockIdx.x);
   const int64_t lh = blockIdx.y;
@@ -134,13 +145,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (bad) atomicOr(a.status, CMR_DEVICE_BAD_CU_SEQLENS);
     if (it.rows > 0 && it.cut) atomicOr(a.status, CMR_DEVICE_CACHE_RANGE);
   }
-  if (it.rows == 0) return;
   const int vis_first = static_cast<int>(it.vis_first), vis_last = static_cast<int>(it.vis_last);
   const int all = max(1, (vis_last + kTile - 1) / kTile);
   const int share = split_tiles(all, ta.splits);
   const int t0 = blockIdx.z * share;
   const int nt = min(share, all - t0);
-  if (nt <= 0) return;
+  if (it.rows == 0 || nt <= 0) {
+    __syncthreads();
+    if (warp == 1) tc::dealloc(*s_tmem, kColumns);
+    return;
+  }
   const bool whole = share == all;
   const int l = static_cast<int>(lh / a.pool.hk), h = static_cast<int>(lh - l * a.pool.hk);
 
@@ -150,18 +164,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       tma::mbar_init(k_empty + 8 * s, 1);
       tma::mbar_init(v_full + 8 * s, 1);
       tma::mbar_init(v_empty + 8 * s, 1);
+      tma::mbar_init(v_clean + 8 * s, kCleaners / 32);
     }
     for (int s = 0; s < 2; ++s) {
       tma::mbar_init(s_full + 8 * s, 2);
       tma::mbar_init(p_full + 8 * s, kSoftmax / 32);
     }
-    tma::mbar_init(o_done, 1);
+    tma::mbar_init(o_done, 2);
     tma::mbar_init(drained, 1);
     tma::mbar_init(q_ready, kSoftmax / 32);
     tma::mbar_init_fence();
     *s_dead = 0;
+    *s_nan_taken = 0;
   }
-  if (warp == 1) tc::alloc(tma::smem_addr(s_tmem), kColumns);
+  for (int d = tid; d < D; d += kThreads) s_nan[d] = 0x7fffffff;
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
@@ -170,7 +186,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // A wait that gives up after its limit ends all later waits of the CTA.
   auto wait = [&](uint32_t bar, int parity) {
-    if (*s_dead) return;
+    if (tma::mbar_try_wait(bar, static_cast<uint32_t>(parity) & 1u) || *s_dead) return;
     if (!tma::mbar_wait(bar, static_cast<uint32_t>(parity) & 1u)) *s_dead = 1;
   };
 
@@ -252,44 +268,67 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       constexpr uint32_t kQkDesc = tc::instruction(tc::kE4M3, tc::kE4M3, false, kTile);
       constexpr uint32_t kPvDesc = tc::instruction(tc::kE5M2, tc::kE4M3, true, D);
+      // The products are issued from straight code, with descriptors that differ by
+      // constants: computed in a loop, each cost about 40 cycles of the tensor pipe.
+      const uint64_t q_desc = tc::descriptor<W>(q_smem, 0, 8 * W);
+      uint64_t k_desc[kStages], v_desc[kStages];
+#pragma unroll
+      for (int s = 0; s < kStages; ++s) {
+        k_desc[s] = tc::descriptor<W>(k_smem + s * S::kTileBytes, 0, 8 * W);
+        v_desc[s] = tc::descriptor<W>(v_smem + s * S::kTileBytes, S::kPanel, 8 * W);
+      }
+      auto keys = [&](int i, int stage, uint64_t kd) {
+        wait(k_full + 8 * stage, i / kStages);
+        tc::fence_after();
+        if (*s_dead) return;
+        tma::mbar_arrive(s_full + 8 * (i & 1));  // passes on what the loads wrote beside
+#pragma unroll
+        for (int term = 0; term < 2; ++term)
+#pragma unroll
+          for (int k = 0; k < D / 32; ++k) {
+            const uint32_t at = (k * 32 / W) * S::kPanel + (k * 32) % W;
+            tc::mma_ss(tmem_s[i & 1], q_desc + ((term * kRows * D + at) >> 4), kd + (at >> 4),
+                       kQkDesc, term + k > 0);
+          }
+        tc::commit(k_empty + 8 * stage);
+        tc::commit(s_full + 8 * (i & 1));
+      };
+      auto values = [&](int j, int stage, uint64_t vd) {
+        wait(v_full + 8 * stage, j / kStages);
+        wait(v_clean + 8 * stage, j / kStages);
+        wait(p_full + 8 * (j & 1), j / 2);
+        tc::fence_after();
+        if (*s_dead) return;
+        tma::mbar_arrive(o_done);  // passes on which NaNs were taken out
+        const uint32_t p = tmem_s[j & 1];
+        // groups of 32 tokens that some row sees
+        const int steps = min(kTile / 32, (vis_last - (t0 + j) * kTile + 31) / 32);
+        if (steps == kTile / 32) {
+#pragma unroll
+          for (int term = 0; term < 3; ++term)
+#pragma unroll
+            for (int k = 0; k < kTile / 32; ++k)
+              tc::mma_ts(tmem, p + term * 32 + k * 8, vd + ((k * 32 * W) >> 4), kPvDesc,
+                         term + k > 0 || j > 0);
+        } else {
+          for (int term = 0; term < 3; ++term)
+            for (int k = 0; k < max(1, steps); ++k)
+              tc::mma_ts(tmem, p + term * 32 + k * 8, vd + ((k * 32 * W) >> 4), kPvDesc,
+                         term + k > 0 || j > 0);
+        }
+        tc::commit(v_empty + 8 * stage);
+        tc::commit(o_done);
+      };
+      static_assert(kStages == 2, "the loop below takes the stages in turn");
       wait(q_ready, 0);
       tc::fence_after();
-      for (int i = 0; i <= nt; ++i) {
+      keys(0, 0, k_desc[0]);
+      for (int i = 1; i <= nt; i += 2) {
+        if (i < nt) keys(i, 1, k_desc[1]);
+        values(i - 1, 0, v_desc[0]);
         if (i < nt) {
-          const int stage = i % kStages;
-          wait(k_full + 8 * stage, i / kStages);
-          tc::fence_after();
-          if (!*s_dead) {
-            tma::mbar_arrive(s_full + 8 * (i & 1));  // passes on what the loads wrote beside
-            for (int term = 0; term < 2; ++term)
-              for (int k = 0; k < D / 32; ++k) {
-                const uint32_t at = (k * 32 / W) * S::kPanel + (k * 32) % W;
-                tc::mma_ss(tmem_s[i & 1],
-                           tc::descriptor<W>(q_smem + term * kRows * D + at, 0, 8 * W),
-                           tc::descriptor<W>(k_smem + stage * S::kTileBytes + at, 0, 8 * W),
-                           kQkDesc, term + k > 0);
-              }
-            tc::commit(k_empty + 8 * stage);
-            tc::commit(s_full + 8 * (i & 1));
-          }
-        }
-        if (i > 0) {
-          const int j = i - 1, stage = j % kStages;
-          wait(v_full + 8 * stage, j / kStages);
-          wait(p_full + 8 * (j & 1), j / 2);
-          tc::fence_after();
-          if (!*s_dead) {
-            // groups of 32 tokens that some row sees
-            const int steps = max(1, min(kTile / 32, (vis_last - (t0 + j) * kTile + 31) / 32));
-            for (int term = 0; term < 3; ++term)
-              for (int k = 0; k < steps; ++k)
-                tc::mma_ts(tmem, tmem_s[j & 1] + term * 32 + k * 8,
-                           tc::descriptor<W>(v_smem + stage * S::kTileBytes + k * 32 * W,
-                                             S::kPanel, 8 * W),
-                           kPvDesc, j + term + k > 0);
-            tc::commit(v_empty + 8 * stage);
-            tc::commit(o_done);
-          }
+          if (i + 1 < nt) keys(i + 1, 0, k_desc[0]);
+          values(i, 1, v_desc[1]);
         }
       }
       // nothing of the tensor cores is in flight when tensor memory is freed
@@ -299,71 +338,138 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp >= kFirstWarp) {
+  } else if (warp < kFirstWarp) {
+    // ---- values that some row does not see.  A weight of zero does not make a NaN
+    // vanish: rows that nobody sees are cleared, and a NaN that some query rows see
+    // and some do not is taken out and given back, at the end, to those that see it.
+    const int ct = tid - 64;
+    for (int i = 0; i < nt; ++i) {
+      const int tile = (t0 + i) * kTile, stage = i % kStages;
+      wait(v_full + 8 * stage, i / kStages);
+      const uint32_t valid = s_info[i % kInfos].valid;
+      if (tile + kTile > vis_first || valid != 0xffu) {
+        uint8_t* v = smem + S::kV + stage * S::kTileBytes;
+        // rows before the first that somebody does not see are fine, and those behind
+        // the last group of 32 that somebody sees take no part
+        const int lo = valid == 0xffu ? max(0, vis_first - tile) : 0;
+        const int hi = min(kTile, (max(vis_last - tile, 1) + 31) / 32 * 32);
+        constexpr int kChunks = D / 16;  // of a row
+        constexpr int kAhead = 8;
+        for (int i0 = lo * kChunks + ct; i0 < hi * kChunks; i0 += kCleaners * kAhead) {
+          uint4 y[kAhead];
+          uint32_t nan = 0;  // chunks that hold one
+#pragma unroll
+          for (int k = 0; k < kAhead; ++k) {
+            const int idx = min(i0 + k * kCleaners, hi * kChunks - 1), r = idx / kChunks;
+            y[k] = *reinterpret_cast<const uint4*>(
+                v + idx % kChunks / (W / 16) * S::kPanel + r * W + idx % (W / 16) * 16);
+          }
+#pragma unroll
+          for (int k = 0; k < kAhead; ++k) {
+            const int idx = i0 + k * kCleaners, r = idx / kChunks;
+            const bool gone = tile + r >= vis_last || !((valid >> (r / 16 & 7)) & 1u);
+            const uint32_t any = nan_codes(y[k].x) | nan_codes(y[k].y) | nan_codes(y[k].z) |
+                                 nan_codes(y[k].w);
+            if (idx < hi * kChunks && gone)
+              *reinterpret_cast<uint4*>(v + idx % kChunks / (W / 16) * S::kPanel + r * W +
+                                        idx % (W / 16) * 16) = make_uint4(0, 0, 0, 0);
+            else if (idx < hi * kChunks && any && tile + r >= vis_first)
+              nan |= 1u << k;
+          }
+          while (nan) {
+            const int idx = i0 + (__ffs(nan) - 1) * kCleaners, r = idx / kChunks;
+            nan &= nan - 1;
+            *s_nan_taken = 1;
+            uint32_t* w = reinterpret_cast<uint32_t*>(
+                v + idx % kChunks / (W / 16) * S::kPanel + r * W + idx % (W / 16) * 16);
+            // logical chunk of this place: the swizzle is its own inverse
+            const int c = (swizzled<W>(r, idx % (W / 16)) - r * W) / 16;
+            const int d = idx % kChunks / (W / 16) * W + c * 16;
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t bad = nan_codes(w[k]);
+              for (int b = 0; b < 4; ++b)
+                if (bad & (0x80u << (8 * b))) atomicMin(&s_nan[d + 4 * k + b], tile + r);
+              w[k] &= ~((bad >> 7) * 0xffu);
+            }
+          }
+        }
+        tma::fence_async_shared();
+      }
+      __syncwarp();
+      if (lane == 0) tma::mbar_arrive(v_clean + 8 * stage);
+    }
+  } else {
     // ---- softmax: thread (row, half)
     const int st = tid - 32 * kFirstWarp;
     const int half = st / kRows, row = st % kRows;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    auto row_at = [&](int r) {
-      const int f = it.first_row + r;
+    if (half == 0) {
+      const int f = it.first_row + row;
       const int64_t tok = it.tok + f / a.group;
-      return ((l * a.batch.n_tokens + tok) * a.hq + h * a.group + f % a.group) * D;
-    };
-    for (int d = st; d < D; d += kSoftmax) s_nan[d] = 0x7fffffff;
+      s_at[row] = ((l * a.batch.n_tokens + tok) * a.hq + h * a.group + f % a.group) * D;
+    }
+    tma::named_sync(1, kSoftmax);
 
-    // Q over a power of two, as two e4m3 terms
-    float mult;
+    // Q over a power of two, as two e4m3 terms: a warp reads whole rows, a 16-byte
+    // chunk (8 dims) to a lane
     {
-      constexpr int kChunks = D / 2 / 8;  // 16-byte chunks of a half row
-      uint4 x[kChunks];
-      uint32_t mx = 0;
-      const uint4* src = reinterpret_cast<const uint4*>(a.q + row_at(row) + half * (D / 2));
+      constexpr int kLanes = D / 8;         // lanes of a row
+      constexpr int kAtOnce = 32 / kLanes;  // rows of a warp's load
+      constexpr int kLoads = kRows / (kSoftmax / 32) / kAtOnce;
+      constexpr int kAhead = kLoads < 16 ? kLoads : 16;
+      const int c = lane % kLanes, first = (warp - kFirstWarp) * kAtOnce + lane / kLanes;
 #pragma unroll
-      for (int c = 0; c < kChunks; ++c) {
-        x[c] = row < it.rows ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
-        const uint32_t w[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+      for (int n0 = 0; n0 < kLoads; n0 += kAhead) {
+        uint4 x[kAhead];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) mx = __vmaxs2(mx, w[i] & 0x7fff7fffu);
-      }
-      mx = max(mx & 0xffffu, mx >> 16);
-      s_max[half * kRows + row] = __uint_as_float(mx);
-      tma::named_sync(1, kSoftmax);
-      mx = max(mx, __float_as_uint(s_max[(1 - half) * kRows + row]));
-      // s = 2^e with max |q| in (224 s, 448 s]
-      int e = static_cast<int>(mx >> 7) - 127 - 8 + ((mx & 0x7fu) > 0x60u ? 1 : 0);
-      e = mx == 0 ? 0 : max(-126, e);
-      // a negative softmax scale turns q around, so that scores only grow with S
-      const float inv = copysignf(__int_as_float((127 - e) << 23), a.scale_log2);
-      mult = mx < 0x7f80u ? fabsf(a.scale_log2) * __int_as_float((127 + e) << 23)
-                          : __int_as_float(0x7fffffff);  // the row becomes NaN
-#pragma unroll
-      for (int c = 0; c < kChunks; c += 2) {
-        uint32_t t1[4], t2[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint4& y = x[c + i / 2];
-          const uint32_t w0 = i % 2 ? y.z : y.x, w1 = i % 2 ? y.w : y.y;
-          const float q[4] = {bf16_lo(w0) * inv, bf16_hi(w0) * inv, bf16_lo(w1) * inv,
-                              bf16_hi(w1) * inv};
-          const uint32_t a0 = f32_to_e4m3x2(q[0], q[1]), a1 = f32_to_e4m3x2(q[2], q[3]);
-          t1[i] = a0 | (a1 << 16);
-          const uint32_t h0 = e4m3x2_to_f16x2(a0), h1 = e4m3x2_to_f16x2(a1);
-          const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&h0));
-          const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&h1));
-          t2[i] = f32_to_e4m3x2(q[0] - f0.x, q[1] - f0.y) |
-                  (f32_to_e4m3x2(q[2] - f1.x, q[3] - f1.y) << 16);
+        for (int n = 0; n < kAhead; ++n) {
+          const int r = first + (n0 + n) * (kSoftmax / 32) * kAtOnce;
+          x[n] = r < it.rows ? __ldg(reinterpret_cast<const uint4*>(a.q + s_at[r]) + c)
+                             : make_uint4(0, 0, 0, 0);
         }
-        const int d = half * (D / 2) + 8 * c;  // 16 dims
-        const int off = (d / W) * S::kPanel + swizzled<W>(row, (d % W) / 16);
-        *reinterpret_cast<uint4*>(smem + S::kQ + off) = make_uint4(t1[0], t1[1], t1[2], t1[3]);
-        *reinterpret_cast<uint4*>(smem + S::kQ + kRows * D + off) =
-            make_uint4(t2[0], t2[1], t2[2], t2[3]);
+#pragma unroll
+        for (int n = 0; n < kAhead; ++n) {
+          const int r = first + (n0 + n) * (kSoftmax / 32) * kAtOnce;
+          const uint32_t w[4] = {x[n].x, x[n].y, x[n].z, x[n].w};
+          uint32_t mx = 0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) mx = __vmaxs2(mx, w[i] & 0x7fff7fffu);
+          mx = max(mx & 0xffffu, mx >> 16);
+          if constexpr (kLanes == 32) {
+            mx = __reduce_max_sync(~0u, mx);
+          } else {
+#pragma unroll
+            for (int o = kLanes / 2; o > 0; o >>= 1) mx = max(mx, __shfl_xor_sync(~0u, mx, o));
+          }
+          // s = 2^e with max |q| in (224 s, 448 s]
+          int e = static_cast<int>(mx >> 7) - 127 - 8 + ((mx & 0x7fu) > 0x60u ? 1 : 0);
+          e = mx == 0 ? 0 : max(-126, e);
+          // a negative softmax scale turns q around, so that scores only grow with S
+          const float inv = copysignf(__int_as_float((127 - e) << 23), a.scale_log2);
+          uint32_t t1[4], t2[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            // exact in f16 down to 2^-14, where e4m3 has 2^-9 for its last bit
+            const uint32_t q = pack_f16x2(bf16_lo(w[i]) * inv, bf16_hi(w[i]) * inv);
+            t1[i] = f16x2_to_e4m3x2(q);
+            t2[i] = f16x2_to_e4m3x2(sub_f16x2(q, e4m3x2_to_f16x2(t1[i])));
+          }
+          const int off = (8 * c / W) * S::kPanel + swizzled<W>(r, (8 * c % W) / 16) + (c & 1) * 8;
+          *reinterpret_cast<uint2*>(smem + S::kQ + off) =
+              make_uint2(t1[0] | (t1[1] << 16), t1[2] | (t1[3] << 16));
+          *reinterpret_cast<uint2*>(smem + S::kQ + kRows * D + off) =
+              make_uint2(t2[0] | (t2[1] << 16), t2[2] | (t2[3] << 16));
+          if (c == 0)
+            s_sum[r] = mx < 0x7f80u ? fabsf(a.scale_log2) * __int_as_float((127 + e) << 23)
+                                    : __int_as_float(0x7fffffff);  // the row becomes NaN
+        }
       }
       tma::fence_async_shared();
       __syncwarp();
       if (lane == 0) tma::mbar_arrive(q_ready);
     }
-    tma::named_sync(1, kSoftmax);  // the rows' maxima have been read
+    tma::named_sync(1, kSoftmax);
+    const float mult = s_sum[row];  // of S, for the exponent (s_sum is free until the end)
     const int seen = row < it.rows
                          ? static_cast<int>(max(static_cast<int64_t>(0),
                                                 min(it.p0 + (it.first_row + row) / a.group + 1,
@@ -470,42 +576,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::st16(tmem_s[i & 1] + lanes + 32 + 16 * half, t2);
       tc::st16(tmem_s[i & 1] + lanes + 64 + 16 * half, t3);
 
-      if (edge) {
-        // A weight of zero does not make a NaN vanish: rows that nobody sees are
-        // cleared, and a NaN that some rows see and some do not is taken out and
-        // given back, at the end, to the rows that see it.
-        const int stage = i % kStages;
-        wait(v_full + 8 * stage, i / kStages);
-        uint8_t* v = smem + S::kV + stage * S::kTileBytes;
-        for (int idx = st; idx < S::kTileBytes / 16; idx += kSoftmax) {
-          const int off = idx * 16;
-          const int r = off % S::kPanel / W;
-          const int tok = tile + r;
-          uint4* at = reinterpret_cast<uint4*>(v + off);
-          if (tok >= vis_last || !((valid >> (r / 16)) & 1u)) {
-            *at = make_uint4(0, 0, 0, 0);
-          } else if (tok >= vis_first) {
-            uint4 y = *at;
-            uint32_t w[4] = {y.x, y.y, y.z, y.w};
-            bool any = false;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint32_t nan = ((w[k] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-              if (nan) {
-                any = true;
-                // logical chunk of this place: the swizzle is its own inverse
-                const int c = (swizzled<W>(r, off % W / 16) - r * W) / 16;
-                const int d = off / S::kPanel * W + c * 16 + 4 * k;
-                for (int b = 0; b < 4; ++b)
-                  if (nan & (0x80u << (8 * b))) atomicMin(&s_nan[d + b], tok);
-                w[k] &= ~((nan >> 7) * 0xffu);
-              }
-            }
-            if (any) *at = make_uint4(w[0], w[1], w[2], w[3]);
-          }
-        }
-        tma::fence_async_shared();
-      }
       tc::wait_st();
       tc::fence_before();
       __syncwarp();
@@ -518,41 +588,69 @@ __global__ void __launch_bounds__(kThreads, 1)
     wait(o_done, nt - 1);
     tc::fence_after();
     const float inv = !whole ? 1.f : (sum == 0.f ? 0.f : 1.f / sum);
-    float* rec = ta.partial +
-                 ((lh * ta.items + bi) * ta.splits + blockIdx.z) * (kRows * (D + 2));
-    if (!whole && half == 0) {
-      rec[kRows * D + row] = ref;
-      rec[kRows * D + kRows + row] = sum;
-    }
+    // Through shared memory, where Q and the keys have been used for the last time,
+    // to rows that a warp writes whole: 16-byte chunks, their place turned by the
+    // row so that neither side meets bank conflicts.
+    const bool nan_taken = *s_nan_taken != 0;
+    const int words = whole ? D / 2 : D;  // of a row: bf16 pairs, or floats
+    const int mask = min(words / 4, 32) - 1;
+    uint32_t* stage = reinterpret_cast<uint32_t*>(smem) + row * words;
 #pragma unroll
     for (int c = 0; c < D / 2; c += 32) {
       uint32_t o[32];
       const int d = half * (D / 2) + c;
       tc::ld32(o, tmem + lanes + d);
       tc::wait_ld();
-      if (row < it.rows) {
 #pragma unroll
-        for (int k = 0; k < 32; ++k) {
-          const float y = __uint_as_float(o[k]) * inv;
-          o[k] = __float_as_uint(s_nan[d + k] < seen ? __int_as_float(0x7fffffff) : y);
+      for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * inv);
+      if (nan_taken) {
+#pragma unroll
+        for (int k = 0; k < 32; ++k)
+          if (s_nan[d + k] < seen) o[k] = 0x7fffffffu;
+      }
+      if (whole) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          uint32_t w[4];
+#pragma unroll
+          for (int m = 0; m < 4; ++m)
+            w[m] = pack_bf16x2(__uint_as_float(o[8 * k + 2 * m]),
+                               __uint_as_float(o[8 * k + 2 * m + 1]));
+          *reinterpret_cast<uint4*>(stage + 4 * ((d / 8 + k) ^ (row & mask))) =
+              make_uint4(w[0], w[1], w[2], w[3]);
         }
-        if (whole) {
-          uint4* dst = reinterpret_cast<uint4*>(a.out + row_at(row) + d);
+      } else {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint32_t w[4];
-#pragma unroll
-            for (int m = 0; m < 4; ++m)
-              w[m] = pack_bf16x2(__uint_as_float(o[8 * k + 2 * m]),
-                                 __uint_as_float(o[8 * k + 2 * m + 1]));
-            dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
-          }
-        } else {
-          uint4* dst = reinterpret_cast<uint4*>(rec + row * D + d);
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            dst[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-        }
+        for (int k = 0; k < 8; ++k)
+          *reinterpret_cast<uint4*>(stage + 4 * ((d / 4 + k) ^ (row & mask))) =
+              make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+      }
+    }
+    float* rec = ta.partial +
+                 ((lh * ta.items + bi) * ta.splits + blockIdx.z) * (kRows * (D + 2));
+    if (!whole && half == 0) {
+      rec[kRows * D + row] = ref;
+      rec[kRows * D + kRows + row] = sum;
+    }
+    tma::named_sync(1, kSoftmax);
+    const uint4* from = reinterpret_cast<const uint4*>(smem);
+    constexpr int kWarps = kSoftmax / 32;
+    if (whole) {
+      constexpr int kChunks = D / 8;        // of a row
+      constexpr int kAtOnce = 32 / kChunks;  // rows of a warp's store
+      const int c = lane % kChunks;
+#pragma unroll 4
+      for (int n = 0; n < kRows / kWarps / kAtOnce; ++n) {
+        const int r = (n * kWarps + warp - kFirstWarp) * kAtOnce + lane / kChunks;
+        if (r < it.rows)
+          reinterpret_cast<uint4*>(a.out + s_at[r])[c] = from[r * kChunks + (c ^ (r & mask))];
+      }
+    } else {
+      constexpr int kChunks = D / 4;
+#pragma unroll 4
+      for (int idx = st; idx < it.rows * kChunks; idx += kSoftmax) {
+        const int r = idx / kChunks, c = idx % kChunks;
+        reinterpret_cast<uint4*>(rec + r * D)[c] = from[r * kChunks + (c ^ (r & mask))];
       }
     }
     tc::fence_before();
@@ -641,6 +739,7 @@ size_t attend_tiles_workspace(int32_t num_seqs, int64_t n_tokens, int32_t num_la
                               int32_t hk, int32_t head_dim) {
   size_t most = 0;
   for (const bool step : {false, true}) {
+    if (step && num_seqs != n_tokens) continue;
     const int64_t items = item_slots(num_seqs, n_tokens, hq / hk, kRows, step) * num_layers * hk;
     const int splits = splits_for(items);
     if (splits == 1) continue;
