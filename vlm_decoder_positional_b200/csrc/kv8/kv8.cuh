@@ -116,6 +116,23 @@ __device__ __forceinline__ bool seq_range(const Batch& b, int32_t i, int64_t& lo
   return false;
 }
 
+// The last i < n with holds(i), holds being true up to some i and false behind it, or
+// 0: asked by a whole warp, 32 places at a time.
+template <typename F>
+__device__ __forceinline__ int32_t last_true(int32_t n, F holds) {
+  int32_t lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int32_t step = (hi - lo + 31) / 32;
+    const int64_t i = lo + static_cast<int64_t>(threadIdx.x & 31) * step;
+    const uint32_t yes = __ballot_sync(~0u, i < hi && holds(static_cast<int32_t>(i)));
+    const int32_t last = yes ? 31 - __clz(yes) : 0;
+    const int64_t next = lo + static_cast<int64_t>(last + 1) * step;
+    lo += last * step;
+    hi = static_cast<int32_t>(next < hi ? next : hi);
+  }
+  return lo;
+}
+
 // Table row of sequence b, or -1 when its slot lies outside the table.
 __device__ __forceinline__ int32_t table_row(const Table& t, int32_t b) {
   const int32_t s = t.slot ? __ldg(t.slot + b) : b;

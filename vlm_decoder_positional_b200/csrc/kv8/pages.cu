@@ -120,7 +120,8 @@ __global__ void __launch_bounds__(kPlanThreads) extend_kernel(const PagesArgs a)
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
   int32_t* need = a.workspace + kHead;  // [n]
   int32_t* have = need + a.n;           // [n]
-  int32_t* list = have + a.n;           // free pages
+  int32_t* first = have + a.n;          // [n]: where its pages start in the list, or -1
+  int32_t* list = first + a.n;          // free pages
   for (int i = warp; i < a.n; i += kPlanWarps) {
     const int32_t slot = __ldg(a.dst + i), len = __ldg(a.lens + i);
     const bool known = slot >= 0 && slot < a.rows && !named_before(a.dst, i, slot);
@@ -161,20 +162,17 @@ __global__ void __launch_bounds__(kPlanThreads) extend_kernel(const PagesArgs a)
     // an entry without enough pages left, and those behind it, get none
     const bool given = at + mine <= free;
     if (mine > 0 && !given) flag(a, CMR_DEVICE_PAGES_FULL);
-    // a warp writes its entries' pages one entry after another
-    uint32_t todo = __ballot_sync(~0u, mine > 0 && given);
-    while (todo) {
-      const int from = __ffs(todo) - 1;
-      todo &= todo - 1;
-      const int e = i0 + warp * 32 + from;
-      const int count = __shfl_sync(~0u, mine, from);
-      const int first = static_cast<int>(__shfl_sync(~0u, at, from));
-      int32_t* row = a.table + static_cast<int64_t>(__ldg(a.dst + e)) * a.max_pages + have[e];
-      for (int k = lane; k < count; k += 32) {
-        const int32_t id = list[first + k];
-        row[k] = id;
-        a.refs[id] = 1;
-      }
+    if (i < a.n) first[i] = given ? static_cast<int32_t>(at) : -1;
+  }
+  __syncthreads();
+  for (int i = warp; i < a.n; i += kPlanWarps) {
+    const int count = need[i], at = first[i];
+    if (count == 0 || at < 0) continue;
+    int32_t* row = a.table + static_cast<int64_t>(__ldg(a.dst + i)) * a.max_pages + have[i];
+    for (int k = lane; k < count; k += 32) {
+      const int32_t id = list[at + k];
+      row[k] = id;
+      a.refs[id] = 1;
     }
   }
 }
@@ -231,29 +229,27 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const PagesArgs
     before += static_cast<int>(sum);
     const bool given = kind == 0 || (kind == 1 && at < free);
     if (kind == 1 && !given) flag(a, CMR_DEVICE_PAGES_FULL);
-    uint32_t todo = __ballot_sync(~0u, given);
-    while (todo) {
-      const int from = __ffs(todo) - 1;
-      todo &= todo - 1;
-      const int e = i0 + warp * 32 + from;
-      const int rank = __shfl_sync(~0u, at, from);
-      const int own = __shfl_sync(~0u, kind, from);
-      const int len = __ldg(a.lens + e);
-      const int32_t* srow = a.table + static_cast<int64_t>(__ldg(a.src + e)) * a.max_pages;
-      int32_t* drow = a.table + static_cast<int64_t>(__ldg(a.dst + e)) * a.max_pages;
-      for (int k = lane; k < len / P; k += 32) {
-        const int32_t id = __ldcg(srow + k);
-        drow[k] = id;
-        atomicAdd(a.refs + id, 1);
-      }
-      if (own && lane == 0) {
-        const int32_t id = list[rank];
-        drow[len / P] = id;
-        a.refs[id] = 1;
-        jobs[3 * rank] = __ldcg(srow + len / P);
-        jobs[3 * rank + 1] = id;
-        jobs[3 * rank + 2] = len % P;
-      }
+    if (i < a.n) state[i] = !given ? -1 : (kind == 1 ? at : a.n);
+  }
+  __syncthreads();
+  for (int i = warp; i < a.n; i += kPlanWarps) {
+    const int rank = state[i];  // among the entries that get a page; n: needs none
+    if (rank < 0) continue;
+    const int len = __ldg(a.lens + i);
+    const int32_t* srow = a.table + static_cast<int64_t>(__ldg(a.src + i)) * a.max_pages;
+    int32_t* drow = a.table + static_cast<int64_t>(__ldg(a.dst + i)) * a.max_pages;
+    for (int k = lane; k < len / P; k += 32) {
+      const int32_t id = __ldcg(srow + k);
+      drow[k] = id;
+      atomicAdd(a.refs + id, 1);
+    }
+    if (rank < a.n && lane == 0) {
+      const int32_t id = list[rank];
+      drow[len / P] = id;
+      a.refs[id] = 1;
+      jobs[3 * rank] = __ldcg(srow + len / P);
+      jobs[3 * rank + 1] = id;
+      jobs[3 * rank + 2] = len % P;
     }
   }
   if (threadIdx.x == 0) a.workspace[kJobs] = min(total, free);

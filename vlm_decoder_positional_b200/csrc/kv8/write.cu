@@ -47,11 +47,18 @@ __device__ __forceinline__ float pow2f(int e) { return __int_as_float((e + 127) 
 // Largest magnitude bits of the two halves of a packed running maximum.
 __device__ __forceinline__ uint32_t halves_max(uint32_t m) { return max(m & 0xffffu, m >> 16); }
 
+// The larger of two packed pairs of bf16 magnitudes; a NaN stays.
+__device__ __forceinline__ uint32_t max_magnitudes(uint32_t m, uint32_t x) {
+  const __nv_bfloat162 r = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&m),
+                                       __habs2(*reinterpret_cast<const __nv_bfloat162*>(&x)));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
 __device__ __forceinline__ uint32_t magnitudes(uint32_t m, const uint4& x) {
-  m = __vmaxs2(m, x.x & 0x7fff7fffu);
-  m = __vmaxs2(m, x.y & 0x7fff7fffu);
-  m = __vmaxs2(m, x.z & 0x7fff7fffu);
-  return __vmaxs2(m, x.w & 0x7fff7fffu);
+  m = max_magnitudes(m, x.x);
+  m = max_magnitudes(m, x.y);
+  m = max_magnitudes(m, x.z);
+  return max_magnitudes(m, x.w);
 }
 
 // The same with infinities and NaN left out.
@@ -65,24 +72,22 @@ __device__ __forceinline__ uint32_t finite_magnitudes(uint32_t m, const uint4& x
   return m;
 }
 
-__device__ __forceinline__ float inf_to_nan(float x) {
-  return fabsf(x) == __int_as_float(0x7f800000) ? __int_as_float(0x7fffffff) : x;
+__device__ __forceinline__ uint4 infs_to_nan(const uint4& x) {
+  uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if ((w[i] & 0x7fffu) == 0x7f80u) w[i] |= 0x40u;
+    if ((w[i] & 0x7fff0000u) == 0x7f800000u) w[i] |= 0x400000u;
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // Eight bf16 values over the scale, as codes.
-template <bool kCheck>
 __device__ __forceinline__ uint2 encode8(const uint4& x, float inv) {
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
   uint32_t r[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float lo = bf16_lo(w[i]), hi = bf16_hi(w[i]);
-    if (kCheck) {
-      lo = inf_to_nan(lo);
-      hi = inf_to_nan(hi);
-    }
-    r[i] = f32_to_e4m3x2(lo * inv, hi * inv);
-  }
+  for (int i = 0; i < 4; ++i) r[i] = f32_to_e4m3x2(bf16_lo(w[i]) * inv, bf16_hi(w[i]) * inv);
   return make_uint2(r[0] | (r[1] << 16), r[2] | (r[3] << 16));
 }
 
@@ -92,6 +97,24 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t w, float ratio) {
   const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&a));
   const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&b));
   return f32_to_e4m3x2(x.x * ratio, x.y * ratio) | (f32_to_e4m3x2(y.x * ratio, y.y * ratio) << 16);
+}
+
+// n16 chunks of 16 codes under another scale, by threads tid of `threads`, four
+// chunks in flight.
+__device__ __forceinline__ void rescale_rows(uint8_t* codes, int n16, float ratio, int tid,
+                                             int threads) {
+  uint4* p = reinterpret_cast<uint4*>(codes);
+  for (int k0 = tid; k0 < n16; k0 += 4 * threads) {
+    uint4 x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (k0 + i * threads < n16) x[i] = p[k0 + i * threads];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (k0 + i * threads < n16)
+        p[k0 + i * threads] = make_uint4(rescale4(x[i].x, ratio), rescale4(x[i].y, ratio),
+                                         rescale4(x[i].z, ratio), rescale4(x[i].w, ratio));
+  }
 }
 
 // The scale of a page whose new rows need exponent e and which held rows under
@@ -143,9 +166,11 @@ __device__ __forceinline__ uint4 rotate_chunk(const uint4& x, int lane, int c, i
   return r;
 }
 
-__device__ __forceinline__ float2 cos_sin_of(const WriteArgs& a, int32_t b, int64_t p, int plane,
-                                             double inv) {
-  const Planes r = canvas_row(p, __ldg(a.start + b), __ldg(a.amount + b));
+__device__ __forceinline__ Planes planes_of(const WriteArgs& a, int32_t b, int64_t p) {
+  return canvas_row(p, __ldg(a.start + b), __ldg(a.amount + b));
+}
+
+__device__ __forceinline__ float2 cos_sin_of(const Planes& r, int plane, double inv) {
   float c, s;
   cos_sin(plane == 0 ? r.t : (plane == 1 ? r.h : r.w), inv, c, s);
   return make_float2(c, s);
@@ -189,10 +214,11 @@ __device__ __forceinline__ void rotate_q_items(const WriteArgs& a, const double*
     p = t - t0;
   }
   p += a.batch.pos_offset ? __ldg(a.batch.pos_offset + b) : 0;
+  const Planes at = planes_of(a, b, p);
   float c[8], s[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const float2 f = cos_sin_of(a, b, p, s_plane[8 * u + e], s_inv[8 * u + e]);
+    const float2 f = cos_sin_of(at, s_plane[8 * u + e], s_inv[8 * u + e]);
     c[e] = f.x;
     s[e] = f.y;
   }
@@ -227,18 +253,158 @@ __device__ __forceinline__ void rotate_q_items(const WriteArgs& a, const double*
   }
 }
 
-template <int D, int P>
-__global__ void __launch_bounds__(kThreads, P * D <= 64 * 256 ? 2 : 1)
-    write_pages_kernel(const WriteArgs a, const FreqTable table, int32_t units, int32_t groups,
-                       int32_t layers_per_group, int32_t q_groups, int32_t q_per_group) {
-  constexpr int D8 = D / 8;                       // 16-byte chunks of a row
-  constexpr int kRows = kThreads / D8;            // rows of one pass
-  constexpr int kPasses = P / kRows > 0 ? P / kRows : 1;
+// Where a CTA's tiles are read and written.
+struct PageWork {
+  const uint16_t* src;  // K or V at the page's first new token, layer 0, head 0
+  uint8_t* codes;       // the pool
+  float* scales;
+  int32_t id, row0, n;  // page, rows it held before, rows to write
+  int64_t tok_stride, layer;  // elements
+  const float2* cs;     // [n][F] (keys)
+};
+
+// Tiles [lo, hi) of K (or of V), a tile being layer t / hk and head t % hk.  A thread
+// holds pairs of 16-byte chunks.  Those that rotation pairs, U = rot_dim / 16 of each
+// row, come first for all rows, so that whole warps rotate or do not; the others are
+// chunks (2 U + c, 2 U + c + left), c < left.  kFull: the whole page is written.
+template <int D, int P, bool kKey, bool kFull>
+__device__ __forceinline__ void write_tiles(const WriteArgs& a, const PageWork& w, int lo, int hi,
+                                            uint32_t (*s_max)[kThreads / 32]) {
+  constexpr int kHalf = D / 16;
+  constexpr int kPairs = P * kHalf / kThreads > 0 ? P * kHalf / kThreads : 1;
   constexpr int kWarps = kThreads / 32;
-  extern __shared__ float2 s_cs[];                // [rows written][F]
+  constexpr bool kAll = kFull && P * kHalf >= kThreads;  // every thread has all its pairs
+  const int lane = threadIdx.x & 31;
+  const int hk = a.pool.hk;
+  const int F = a.rot_dim / 2;
+  const int U = kKey ? F / 8 : 0, left = kHalf - U;
+  const int turned = w.n * U;  // rotated pairs
+  int from[kPairs];            // element offset of the first chunk, -1: no pair
+  uint32_t to[kPairs];         // byte offset in the page
+  int cs[kPairs];              // of the pair's cos/sin
+  if constexpr (kKey) {
+    const int reciprocal = left > 0 ? ((1 << 20) + left - 1) / left : 0;
+#pragma unroll
+    for (int k = 0; k < kPairs; ++k) {
+      const int idx = threadIdx.x + k * kThreads, rest = idx - turned;
+      // rest < 2,048 and left <= 16: the product is below 2^31 and the quotient exact
+      const int r = idx < turned ? idx / max(U, 1) : (rest * reciprocal) >> 20;
+      const int c = idx < turned ? idx - r * U : 2 * U + rest - r * left;
+      from[k] = kAll || idx < w.n * kHalf ? static_cast<int>(r * w.tok_stride) + 8 * c : -1;
+      to[k] = (w.row0 + r) * D + 8 * c;
+      cs[k] = r * F + 8 * c;
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < kPairs; ++k) {
+      const int idx = threadIdx.x + k * kThreads, r = idx / kHalf, c = idx % kHalf;
+      from[k] = kAll || r < w.n ? static_cast<int>(r * w.tok_stride) + 8 * c : -1;
+      to[k] = (w.row0 + r) * D + 8 * c;
+      cs[k] = 0;
+    }
+  }
+  const bool held = w.row0 > 0;
+  for (int m = lo; m < hi; ++m) {
+    const int l = m / hk, h = m - l * hk;
+    const uint16_t* src = w.src + l * w.layer + h * D;
+    const int64_t at = unit_index(a.pool, l, w.id, h);
+    const float old = held ? __ldcg(w.scales + at) : 0.f;
+    uint4 x[kPairs][2];
+#pragma unroll
+    for (int k = 0; k < kPairs; ++k) {
+      const int apart = kKey && threadIdx.x + k * kThreads < turned ? U : left;
+      if (kAll || from[k] >= 0) {
+        const uint4* p = reinterpret_cast<const uint4*>(src + from[k]);
+        x[k][0] = __ldcs(p);
+        x[k][1] = __ldcs(p + apart);
+      } else {
+        x[k][0] = x[k][1] = make_uint4(0, 0, 0, 0);
+      }
+    }
+    uint32_t mx = 0;
+#pragma unroll
+    for (int k = 0; k < kPairs; ++k) {
+      if (kKey && threadIdx.x + k * kThreads < turned) {
+        const float4* f = reinterpret_cast<const float4*>(w.cs + cs[k]);
+        float c[8], s[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float4 y = f[e];
+          c[2 * e] = y.x;
+          s[2 * e] = y.y;
+          c[2 * e + 1] = y.z;
+          s[2 * e + 1] = y.w;
+        }
+        rotate_unit(x[k][0], x[k][1], c, s);
+      }
+      mx = magnitudes(magnitudes(mx, x[k][0]), x[k][1]);
+    }
+    mx = __reduce_max_sync(~0u, halves_max(mx));
+    if (lane == 0) s_max[m & 1][threadIdx.x / 32] = mx;
+    __syncthreads();  // the next tile's maxima go to the other half
+    uint32_t bits = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) bits = max(bits, s_max[m & 1][i]);
+    const bool odd_values = bits >= 0x7f80u;  // an infinity or a NaN
+    if (odd_values) {
+      mx = 0;
+#pragma unroll
+      for (int k = 0; k < kPairs; ++k)
+        mx = finite_magnitudes(finite_magnitudes(mx, x[k][0]), x[k][1]);
+      mx = __reduce_max_sync(~0u, halves_max(mx));
+      __syncthreads();
+      if (lane == 0) s_max[m & 1][threadIdx.x / 32] = mx;
+      __syncthreads();
+      bits = 0;
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i) bits = max(bits, s_max[m & 1][i]);
+    }
+    float ratio;
+    const float s = page_scale(scale_exp(bits), held, old, &ratio, a.status);
+    const float inv = 1.f / s;
+    uint8_t* page = w.codes + at * (P * D);
+    if (odd_values) {
+#pragma unroll
+      for (int k = 0; k < kPairs; ++k) {
+        x[k][0] = infs_to_nan(x[k][0]);
+        x[k][1] = infs_to_nan(x[k][1]);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kPairs; ++k) {
+      const int apart = kKey && threadIdx.x + k * kThreads < turned ? U : left;
+      if (kAll || from[k] >= 0) {
+        uint2* dst = reinterpret_cast<uint2*>(page + to[k]);
+        __stcs(dst, encode8(x[k][0], inv));
+        __stcs(dst + apart, encode8(x[k][1], inv));
+      }
+    }
+    if (ratio != 1.f) rescale_rows(page, w.row0 * (D / 16), ratio, threadIdx.x, kThreads);
+    if (threadIdx.x == 0) w.scales[at] = s;
+  }
+}
+
+template <int D, int P, bool kKey>
+__device__ __forceinline__ void write_tiles(const WriteArgs& a, const PageWork& w, int lo, int hi,
+                                            uint32_t (*s_max)[kThreads / 32]) {
+  if (w.n == P)
+    write_tiles<D, P, kKey, true>(a, w, lo, hi, s_max);
+  else
+    write_tiles<D, P, kKey, false>(a, w, lo, hi, s_max);
+}
+
+// Tiles of a page: its K, then its V, each layer by layer, head by head.
+template <int D, int P>
+__global__ void __launch_bounds__(kThreads, P * D <= 64 * 256 ? 3 : 2)
+    write_pages_kernel(const WriteArgs a, const FreqTable table, int32_t units, int32_t groups,
+                       int32_t tiles_per_group, int32_t q_groups, int32_t q_per_group) {
+  constexpr int kWarps = kThreads / 32;
+  extern __shared__ float4 s_cs4[];               // [rows written][F] of (cos, sin)
   __shared__ double s_inv[kMaxFreqs];
   __shared__ int32_t s_plane[kMaxFreqs];
   __shared__ uint32_t s_max[2][kWarps];
+  __shared__ Planes s_at[P];                      // of the rows written
+  float2* s_cs = reinterpret_cast<float2*>(s_cs4);
   const int F = a.rot_dim / 2;
   for (int j = threadIdx.x; j < F; j += kThreads) {
     s_inv[j] = table.inv_freq[j];
@@ -252,21 +418,15 @@ __global__ void __launch_bounds__(kThreads, P * D <= 64 * 256 ? 2 : 1)
     return;
   }
   const int32_t unit = blockIdx.x / groups;
-  const int l_lo = (blockIdx.x - unit * groups) * layers_per_group;
-  const int l_hi = min(a.pool.num_layers, l_lo + layers_per_group);
+  const int hk = a.pool.hk;
+  const int k_tiles = a.pool.num_layers * hk;
+  const int m_lo = (blockIdx.x - unit * groups) * tiles_per_group;
+  const int m_hi = min(2 * k_tiles, m_lo + tiles_per_group);
 
   // The sequence of this unit: the last b with cu[b] / P + 2 b <= unit.
-  int32_t b = 0;
-  {
-    int32_t hi = a.batch.num_seqs;
-    while (hi - b > 1) {
-      const int32_t mid = (b + hi) >> 1;
-      if (__ldg(a.batch.cu + mid) / P + 2 * static_cast<int64_t>(mid) <= unit)
-        b = mid;
-      else
-        hi = mid;
-    }
-  }
+  const int32_t b = last_true(a.batch.num_seqs, [&](int32_t i) {
+    return __ldg(a.batch.cu + i) / P + 2 * static_cast<int64_t>(i) <= unit;
+  });
   int64_t t0, t1;
   if (!seq_range(a.batch, b, t0, t1)) {
     if (threadIdx.x == 0 && a.status != nullptr) atomicOr(a.status, CMR_DEVICE_BAD_CU_SEQLENS);
@@ -289,96 +449,35 @@ __global__ void __launch_bounds__(kThreads, P * D <= 64 * 256 ? 2 : 1)
   const int row0 = static_cast<int>(first - j * P);  // rows the page held before
   const int n = static_cast<int>(last - first);      // rows to write
   const int64_t tok = t0 + (first - p0);
-  for (int m = threadIdx.x; m < n * F; m += kThreads) {
-    const int r = m / F, f = m - r * F;
-    s_cs[m] = cos_sin_of(a, b, first + r, s_plane[f], s_inv[f]);
+  if (m_lo < k_tiles) {
+    for (int r = threadIdx.x; r < n; r += kThreads) s_at[r] = planes_of(a, b, first + r);
+    __syncthreads();
+    for (int m = threadIdx.x; m < n * F; m += kThreads) {
+      const int r = m / F, f = m - r * F;
+      s_cs[m] = cos_sin_of(s_at[r], s_plane[f], s_inv[f]);
+    }
+    __syncthreads();
   }
-  __syncthreads();
 
-  const int lane = threadIdx.x & 31;
-  const int c = threadIdx.x % D8, r0 = threadIdx.x / D8;
-  const int half8 = F / 8;
-  const int hk = a.pool.hk;
-  const int64_t tok_stride = static_cast<int64_t>(hk) * D;
-  const int64_t layer = a.batch.n_tokens * tok_stride;
-  const int tiles = (l_hi - l_lo) * hk * 2;
-  // tile m: layer l_lo + m / (2 hk), K (even) or V (odd) of head (m / 2) % hk
-  auto load = [&](int m, uint4(&x)[kPasses], float& old) {
-    const int l = l_lo + m / (2 * hk), h = (m >> 1) % hk;
-    const uint16_t* src = (m & 1) ? a.v : a.k;
-    const uint4* p = reinterpret_cast<const uint4*>(src + l * layer + tok * tok_stride + h * D) + c;
-#pragma unroll
-    for (int k = 0; k < kPasses; ++k) {
-      const int r = r0 + k * kRows;
-      x[k] = make_uint4(0, 0, 0, 0);
-      if (r < n) x[k] = __ldcs(p + r * (tok_stride / 8));
-    }
-    old = row0 > 0 ? __ldcg(((m & 1) ? a.pool.vs : a.pool.ks) + unit_index(a.pool, l, id, h)) : 0.f;
-  };
-
-  uint4 x[kPasses], next[kPasses];
-  float old, next_old = 0.f;
-  load(0, x, old);
-  for (int m = 0; m < tiles; ++m) {
-    if (m + 1 < tiles) load(m + 1, next, next_old);
-    if ((m & 1) == 0) {
-#pragma unroll
-      for (int k = 0; k < kPasses; ++k) {
-        const int r = r0 + k * kRows;  // rows of zeros turn to zeros
-        x[k] = rotate_chunk(x[k], lane, c, half8, s_cs + (r < n ? r : 0) * F);
-      }
-    }
-    uint32_t mx = 0;
-#pragma unroll
-    for (int k = 0; k < kPasses; ++k) mx = magnitudes(mx, x[k]);
-    mx = __reduce_max_sync(~0u, halves_max(mx));
-    if (lane == 0) s_max[m & 1][threadIdx.x / 32] = mx;
-    __syncthreads();  // the next tile's maxima go to the other half
-    uint32_t bits = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) bits = max(bits, s_max[m & 1][w]);
-    const bool odd_values = bits >= 0x7f80u;  // an infinity or a NaN
-    if (odd_values) {
-      mx = 0;
-#pragma unroll
-      for (int k = 0; k < kPasses; ++k) mx = finite_magnitudes(mx, x[k]);
-      mx = __reduce_max_sync(~0u, halves_max(mx));
-      __syncthreads();
-      if (lane == 0) s_max[m & 1][threadIdx.x / 32] = mx;
-      __syncthreads();
-      bits = 0;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) bits = max(bits, s_max[m & 1][w]);
-    }
-    const int l = l_lo + m / (2 * hk), h = (m >> 1) % hk;
-    const int64_t at = unit_index(a.pool, l, id, h);
-    float ratio;
-    const float s = page_scale(scale_exp(bits), row0 > 0, old, &ratio, a.status);
-    const float inv = 1.f / s;
-    uint8_t* page = ((m & 1) ? a.pool.v : a.pool.k) + at * (P * D);
-    uint2* dst = reinterpret_cast<uint2*>(page + row0 * D) + c;
-    if (!odd_values) {
-#pragma unroll
-      for (int k = 0; k < kPasses; ++k) {
-        const int r = r0 + k * kRows;
-        if (r < n) __stcs(dst + r * D8, encode8<false>(x[k], inv));
-      }
-    } else {
-#pragma unroll
-      for (int k = 0; k < kPasses; ++k) {
-        const int r = r0 + k * kRows;
-        if (r < n) __stcs(dst + r * D8, encode8<true>(x[k], inv));
-      }
-    }
-    if (ratio != 1.f) {
-      uint32_t* held = reinterpret_cast<uint32_t*>(page);
-      for (int k = threadIdx.x; k < row0 * (D / 4); k += kThreads)
-        held[k] = rescale4(held[k], ratio);
-    }
-    if (threadIdx.x == 0) ((m & 1) ? a.pool.vs : a.pool.ks)[at] = s;
-#pragma unroll
-    for (int k = 0; k < kPasses; ++k) x[k] = next[k];
-    old = next_old;
+  PageWork w;
+  w.tok_stride = static_cast<int64_t>(hk) * D;
+  w.layer = a.batch.n_tokens * w.tok_stride;
+  w.id = id;
+  w.row0 = row0;
+  w.n = n;
+  w.cs = s_cs;
+  if (m_lo < k_tiles) {
+    w.src = a.k + tok * w.tok_stride;
+    w.codes = a.pool.k;
+    w.scales = a.pool.ks;
+    write_tiles<D, P, true>(a, w, m_lo, min(m_hi, k_tiles), s_max);
+    __syncthreads();  // the maxima of the last tile have been read
+  }
+  if (m_hi > k_tiles) {
+    w.src = a.v + tok * w.tok_stride;
+    w.codes = a.pool.v;
+    w.scales = a.pool.vs;
+    write_tiles<D, P, false>(a, w, max(m_lo, k_tiles) - k_tiles, m_hi - k_tiles, s_max);
   }
 }
 
@@ -414,8 +513,9 @@ __global__ void __launch_bounds__(kStepThreads)
     xk = __ldcs(reinterpret_cast<const uint4*>(a.k + kv_at) + lane);
     xv = __ldcs(reinterpret_cast<const uint4*>(a.v + kv_at) + lane);
   }
+  const Planes planes = planes_of(a, b, p);
   for (int f = lane; f < F; f += 32)
-    s_cs[warp][f] = cos_sin_of(a, b, p, table.plane[f], table.inv_freq[f]);
+    s_cs[warp][f] = cos_sin_of(planes, table.plane[f], table.inv_freq[f]);
   __syncwarp();
 
   if (is_q) {
@@ -459,12 +559,8 @@ __global__ void __launch_bounds__(kStepThreads)
     const float s = page_scale(scale_exp(bits), row0 > 0, which ? old_v : old_k, &ratio, a.status);
     uint8_t* page = (which ? a.pool.v : a.pool.k) + at * (P * D);
     if (lane < D8)
-      reinterpret_cast<uint2*>(page + row0 * D)[lane] = encode8<true>(x, 1.f / s);
-    if (ratio != 1.f) {
-      uint32_t* held = reinterpret_cast<uint32_t*>(page);
-#pragma unroll 4
-      for (int k = lane; k < row0 * (D / 4); k += 32) held[k] = rescale4(held[k], ratio);
-    }
+      reinterpret_cast<uint2*>(page + row0 * D)[lane] = encode8(infs_to_nan(x), 1.f / s);
+    if (ratio != 1.f) rescale_rows(page, row0 * (D / 16), ratio, lane, 32);
     if (lane == 0) (which ? a.pool.vs : a.pool.ks)[at] = s;
   }
 }
@@ -482,16 +578,24 @@ cudaError_t launch_pages(const WriteArgs& a, const FreqTable& table, cudaStream_
     if (e != cudaSuccess) return e;
   }
   const int L = a.pool.num_layers;
-  const int groups = L;  // one layer to a CTA
+  // Up to eight tiles to a CTA, whose K tiles share their cos/sin, while that leaves
+  // two waves of CTAs; one tile each when there are few pages.
+  const int tiles = 2 * L * a.pool.hk;
+  const int64_t wanted = 2 * 4 * static_cast<int64_t>(sm_count());
+  int per = 8;
+  while (per > 1 && units * ((tiles + per - 1) / per) < wanted) per /= 2;
+  const int groups = (tiles + per - 1) / per;
   int32_t q_groups = 0, q_per = 1;
   int64_t q_blocks = 0;
   if (a.hq > 0) {
     // a token's (layer, head) rows are split while there are too few threads for
-    // two waves of the device
+    // two waves of the device, but eight share a cos/sin, which costs as much as
+    // ten rotated rows
     const int64_t rows = static_cast<int64_t>(a.hq) * L;
     const int64_t per_cta = kThreads / (F / 8);
     const int64_t want = (2 * static_cast<int64_t>(sm_count()) * 4 * per_cta + N - 1) / N;
-    const int64_t g = want < 1 ? 1 : (want > rows ? rows : want);
+    const int64_t most = (rows + 7) / 8;
+    const int64_t g = want < 1 ? 1 : (want > most ? most : want);
     q_per = static_cast<int32_t>((rows + g - 1) / g);
     q_groups = static_cast<int32_t>((rows + q_per - 1) / q_per);
     q_blocks = (N * q_groups + per_cta - 1) / per_cta;
@@ -499,7 +603,7 @@ cudaError_t launch_pages(const WriteArgs& a, const FreqTable& table, cudaStream_
   const int64_t blocks = units * groups + q_blocks;
   if (units > INT32_MAX || blocks > INT32_MAX) return cudaErrorInvalidValue;
   write_pages_kernel<D, P><<<static_cast<unsigned>(blocks), kThreads, smem, stream>>>(
-      a, table, static_cast<int32_t>(units), groups, (L + groups - 1) / groups, q_groups, q_per);
+      a, table, static_cast<int32_t>(units), groups, per, q_groups, q_per);
   return cudaGetLastError();
 }
 
