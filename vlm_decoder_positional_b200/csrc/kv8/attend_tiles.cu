@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tma::mbar_init(s_full + 8 * s, 2);
       tma::mbar_init(p_full + 8 * s, kSoftmax / 32);
     }
-    tma::mbar_init(o_done, 2);
+    tma::mbar_init(o_done, 1);
     tma::mbar_init(drained, 1);
     tma::mbar_init(q_ready, kSoftmax / 32);
     tma::mbar_init_fence();
@@ -281,7 +281,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         wait(k_full + 8 * stage, i / kStages);
         tc::fence_after();
         if (*s_dead) return;
-        tma::mbar_arrive(s_full + 8 * (i & 1));  // passes on what the loads wrote beside
+        // passes on what the loads wrote beside the keys; the buffer's last phase is over,
+        // since its weights were waited for
+        tma::mbar_arrive(s_full + 8 * (i & 1));
 #pragma unroll
         for (int term = 0; term < 2; ++term)
 #pragma unroll
@@ -299,7 +301,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         wait(p_full + 8 * (j & 1), j / 2);
         tc::fence_after();
         if (*s_dead) return;
-        tma::mbar_arrive(o_done);  // passes on which NaNs were taken out
         const uint32_t p = tmem_s[j & 1];
         // groups of 32 tokens that some row sees
         const int steps = min(kTile / 32, (vis_last - (t0 + j) * kTile + 31) / 32);
@@ -398,6 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) tma::mbar_arrive(v_clean + 8 * stage);
     }
+    tma::named_sync(6, kSoftmax + kCleaners);  // which NaNs were taken out is known
   } else {
     // ---- softmax: thread (row, half)
     const int st = tid - 32 * kFirstWarp;
@@ -533,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ref = to;
         sum *= down;
         if (i > 0) {
-          wait(o_done, i - 1);
+          wait(o_done, i - 1);  // S of this tile came after the product of tile i - 2
           tc::fence_after();
 #pragma unroll
           for (int d = 0; d < D / 2; d += 32) {
@@ -583,8 +585,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 
     s_sum[half * kRows + row] = sum;
-    tma::named_sync(1, kSoftmax);
+    tma::named_sync(6, kSoftmax + kCleaners);
     sum += s_sum[(1 - half) * kRows + row];
+    // a phase's parity tells it from its neighbours only: the last product but one may
+    // still be running here, since its keys' successors were multiplied before it
+    if (nt > 1) wait(o_done, nt - 2);
     wait(o_done, nt - 1);
     tc::fence_after();
     const float inv = !whole ? 1.f : (sum == 0.f ? 0.f : 1.f / sum);
