@@ -191,6 +191,14 @@ CMR_API cmr_status cmr_kv8_compact(void* k_pages, void* v_pages, float* k_scales
  * call is made. */
 CMR_API size_t cmr_kv8_pages_workspace_bytes(int32_t table_rows, int32_t num_pages, int32_t n);
 
+/* The calls above with their arguments in an array, one 8-byte word each, in order
+ * and the stream among them (integers and addresses as int64, doubles as they are),
+ * for bindings to which each argument is a cost of its own.
+ *   call   0 cmr_kv8_rotate_qk (28 words), 1 cmr_kv8_attend (25), 2 cmr_kv8_extend (13),
+ *          3 cmr_kv8_fork (21), 4 cmr_kv8_free (9), 5 cmr_kv8_compact (17)
+ * Errors: those of the call, CMR_EINVAL for another number or count of words. */
+CMR_API cmr_status cmr_kv8_call(int32_t call, const void* words, int32_t count);
+
 /* Name of the kernel that the calling thread's last cmr_kv8_attend enqueued
  * ("attend_rows_kernel" or "attend_tiles_kernel"); "" before the first. */
 CMR_API const char* cmr_kv8_last_attend_kernel(void);

@@ -30,7 +30,7 @@ def declared():
 
 def test_header_binding_and_library_agree(lib):
     names = set(declared())
-    assert names == set(kv8.SIGNATURES) and len(names) == 10
+    assert names == set(kv8.SIGNATURES) and len(names) == 11
     out = subprocess.run(["nm", "-D", "--defined-only", libbuild.KV8_LIB], check=True,
                          capture_output=True, text=True).stdout
     exported = {line.split()[-1] for line in out.splitlines() if line.strip()}
@@ -164,6 +164,25 @@ def test_page_calls_of_nothing_are_no_ops(lib):
     assert kv8.kv8_pages_workspace_bytes(0, 4) == 0
     assert kv8.kv8_pages_workspace_bytes(2, 4, -1) == 0
     assert kv8.kv8_pages_workspace_bytes(2, 1000, 8) >= 4 * (1000 * 2 + 8 * 4)
+
+
+def test_calls_by_words_are_the_calls(lib):
+    for name, (number, words) in kv8._CALLS.items():
+        args = kv8.SIGNATURES[name][1]
+        kinds = "".join("d" if a is ctypes.c_double else "q" for a in args)
+        plain = words.format.lstrip("=")
+        spelled = "".join((c[-1] * int(c[:-1] or 1)) for c in re.findall(r"\d*[qd]", plain))
+        assert spelled == kinds, name
+        ok = words.pack(*[0.0 if k == "d" else 0 for k in kinds])
+        assert lib.cmr_kv8_call(number, ok, len(kinds)) in (1, 3)      # zeros: refused
+        assert lib.cmr_kv8_call(number, ok, len(kinds) - 1) == 1
+        assert b"words" in lib.cmr_kv8_last_error_message()
+    assert lib.cmr_kv8_call(6, b"", 0) == 1 and lib.cmr_kv8_call(-1, b"", 0) == 1
+    assert lib.cmr_kv8_call(0, None, 28) == 1
+    # a count that does not fit 32 bits is refused, not cut
+    free = kv8._CALLS["cmr_kv8_free"][1]
+    assert lib.cmr_kv8_call(4, free.pack(FAKE, 2, 2, FAKE, 4, FAKE, 1 << 32, 0, 0), 9) == 1
+    assert b"negative n" in lib.cmr_kv8_last_error_message()
 
 
 def test_python_refuses_what_is_not_on_a_gpu():

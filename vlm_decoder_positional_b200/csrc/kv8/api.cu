@@ -6,6 +6,7 @@
 #include <cstdarg>
 #include <cstdint>
 #include <cstdio>
+#include <cstring>
 #include <mutex>
 
 #include "kv8.cuh"
@@ -37,7 +38,7 @@ cmr_status check(const void* p, const char* name, size_t align = 4, bool optiona
   return CMR_OK;
 }
 
-cmr_status on_device(const void* p, const char* name) {
+cmr_status on_device(const void* p, const char* name, int dev) {
   if (p == nullptr) return CMR_OK;
   cudaPointerAttributes attr;
   cudaError_t e = cudaPointerGetAttributes(&attr, p);
@@ -48,9 +49,6 @@ cmr_status on_device(const void* p, const char* name) {
   if (attr.type != cudaMemoryTypeDevice && attr.type != cudaMemoryTypeManaged)
     return fail(CMR_EINVAL, "%s: not device memory (memory type %d)", name,
                 static_cast<int>(attr.type));
-  int dev = -1;
-  e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
   if (attr.type == cudaMemoryTypeDevice && attr.device != dev)
     return fail(CMR_EINVAL, "%s: lives on device %d but device %d is current", name,
                 attr.device, dev);
@@ -64,8 +62,10 @@ struct Named {
 
 template <size_t N>
 cmr_status all_on_device(const Named (&list)[N]) {
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) cudaGetLastError();  // no pointer will pass then
   for (const Named& x : list) {
-    const cmr_status s = on_device(x.p, x.name);
+    const cmr_status s = on_device(x.p, x.name, dev);
     if (s != CMR_OK) return s;
   }
   return CMR_OK;
@@ -161,9 +161,21 @@ cmr_status check_rotation(double theta, const int32_t sections[3], int32_t rot_d
   if (!(theta > 0.0) || !std::isfinite(theta)) return fail(CMR_EINVAL, "theta must be finite and > 0");
   if (!sections) return fail(CMR_EINVAL, "sections is required");
   const int F = rot_dim / 2;
+  // a model calls with one theta and rot_dim: their powers cost as much as the launch
+  thread_local struct {
+    double theta;
+    int32_t rot_dim;
+    double inv_freq[cmr::kMaxFreqs];
+  } last = {};
+  if (last.theta != theta || last.rot_dim != rot_dim) {
+    for (int j = 0; j < cmr::kMaxFreqs; ++j)
+      last.inv_freq[j] = j < F ? std::pow(theta, -2.0 * j / rot_dim) : 0.0;
+    last.theta = theta;
+    last.rot_dim = rot_dim;
+  }
   for (int j = 0; j < cmr::kMaxFreqs; ++j) {
     table->plane[j] = 0;
-    table->inv_freq[j] = j < F ? std::pow(theta, -2.0 * j / rot_dim) : 0.0;
+    table->inv_freq[j] = last.inv_freq[j];
   }
   if (sections[0] < 0 || sections[1] < 0 || sections[2] < 0 ||
       static_cast<int64_t>(sections[0]) + sections[1] + sections[2] != F)
@@ -202,6 +214,31 @@ cmr_status check_pages_workspace(void* workspace, size_t workspace_bytes,
   return check_workspace(workspace, workspace_bytes,
                          cmr::kv8::pages_workspace_bytes(a->rows, a->pool.num_pages, a->n));
 }
+
+// The words of cmr_kv8_call.
+struct Words {
+  const char* at;
+  int64_t i64(int k) const {
+    int64_t v;
+    memcpy(&v, at + 8 * k, 8);
+    return v;
+  }
+  double f64(int k) const {
+    double v;
+    memcpy(&v, at + 8 * k, 8);
+    return v;
+  }
+  // what does not fit becomes a negative number, which every call refuses
+  int32_t i32(int k) const {
+    const int64_t v = i64(k);
+    return v >= INT32_MIN && v <= INT32_MAX ? static_cast<int32_t>(v) : INT32_MIN;
+  }
+  size_t size(int k) const { return static_cast<size_t>(i64(k)); }
+  void* ptr(int k) const { return reinterpret_cast<void*>(i64(k)); }
+  int32_t* ints(int k) const { return reinterpret_cast<int32_t*>(i64(k)); }
+  float* flt(int k) const { return reinterpret_cast<float*>(i64(k)); }
+  cmr_stream_t stream(int k) const { return reinterpret_cast<cmr_stream_t>(i64(k)); }
+};
 
 }  // namespace
 
@@ -454,6 +491,50 @@ cmr_status cmr_kv8_compact(void* k_pages, void* v_pages, float* k_scales, float*
   a.status = device_status;
   const cudaError_t e = cmr::kv8::launch_compact(a, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? CMR_OK : cuda_fail(e, "kv8_compact launch");
+}
+
+cmr_status cmr_kv8_call(int32_t call, const void* words, int32_t count) {
+  if (!words) return fail(CMR_EINVAL, "words is required");
+  const Words w{static_cast<const char*>(words)};
+  switch (call) {
+    case 0:
+      if (count != 28) break;
+      return cmr_kv8_rotate_qk(w.ptr(0), w.ptr(1), w.ptr(2), w.ints(3), w.i32(4), w.ints(5),
+                               w.ints(6), w.ints(7), w.i64(8), w.i32(9), w.i32(10), w.i32(11),
+                               w.i32(12), w.f64(13), w.ints(14), w.i32(15), w.ptr(16), w.ptr(17),
+                               w.flt(18), w.flt(19), w.i32(20), w.i32(21), w.ints(22), w.i32(23),
+                               w.i32(24), w.ints(25), w.ints(26), w.stream(27));
+    case 1:
+      if (count != 25) break;
+      return cmr_kv8_attend(w.ptr(0), w.ptr(1), w.ints(2), w.i32(3), w.ints(4), w.i64(5),
+                            w.i32(6), w.i32(7), w.i32(8), w.i32(9), w.f64(10), w.ptr(11),
+                            w.ptr(12), w.flt(13), w.flt(14), w.i32(15), w.i32(16), w.ints(17),
+                            w.i32(18), w.i32(19), w.ints(20), w.ptr(21), w.size(22), w.ints(23),
+                            w.stream(24));
+    case 2:
+      if (count != 13) break;
+      return cmr_kv8_extend(w.ints(0), w.i32(1), w.i32(2), w.ints(3), w.i32(4), w.i32(5),
+                            w.ints(6), w.ints(7), w.i32(8), w.ptr(9), w.size(10), w.ints(11),
+                            w.stream(12));
+    case 3:
+      if (count != 21) break;
+      return cmr_kv8_fork(w.ptr(0), w.ptr(1), w.flt(2), w.flt(3), w.i32(4), w.i32(5), w.i32(6),
+                          w.i32(7), w.i32(8), w.ints(9), w.i32(10), w.i32(11), w.ints(12),
+                          w.ints(13), w.ints(14), w.ints(15), w.i32(16), w.ptr(17), w.size(18),
+                          w.ints(19), w.stream(20));
+    case 4:
+      if (count != 9) break;
+      return cmr_kv8_free(w.ints(0), w.i32(1), w.i32(2), w.ints(3), w.i32(4), w.ints(5), w.i32(6),
+                          w.ints(7), w.stream(8));
+    case 5:
+      if (count != 17) break;
+      return cmr_kv8_compact(w.ptr(0), w.ptr(1), w.flt(2), w.flt(3), w.i32(4), w.i32(5), w.i32(6),
+                             w.i32(7), w.i32(8), w.ints(9), w.i32(10), w.i32(11), w.ints(12),
+                             w.ptr(13), w.size(14), w.ints(15), w.stream(16));
+    default:
+      return fail(CMR_EINVAL, "no call has the number %d", call);
+  }
+  return fail(CMR_EINVAL, "call %d does not have %d words", call, count);
 }
 
 }  // extern "C"

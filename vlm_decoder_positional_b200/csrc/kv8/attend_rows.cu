@@ -149,6 +149,18 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? 2 : 1)
     }
     tma::mbar_init_fence();
   }
+  // What the first copies will wait for, one after another, is asked for at once: the
+  // tensor maps, and the page table, a line to a thread of the grid.
+  if (tid == 32) {
+    tma::prefetch_map(&k_map);
+    tma::prefetch_map(&v_map);
+  }
+  {
+    const int64_t line = (static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x) * kThreads + tid;
+    const int64_t entry = line * 32;
+    if (entry < static_cast<int64_t>(a.table.rows) * a.table.max_pages)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(a.table.pages + entry));
+  }
   // ---- the items and this CTA's run [lo, hi) of the work
   bool bad = false;
   const int first = ra.ctas > 0 ? 0 : blockIdx.x;  // item number of list entry 0
@@ -183,13 +195,14 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? 2 : 1)
     if (lane == 0) s_prefix[kept] = carry;
   }
   __syncthreads();
-  const int32_t total = s_prefix[kept];  // per (layer, head)
-  int64_t run_lo, run_hi, lh0 = 0;
+  // per (layer, head); all of the work fits 31 bits, which the launch has seen to
+  const uint32_t total = s_prefix[kept];
+  uint32_t run_lo, run_hi, lh0 = 0;
   if (ra.ctas > 0) {
     if (blockIdx.x == 0)
       for (int i = tid; i <= NB; i += kThreads) ra.prefix[i] = s_prefix[i];
-    const int64_t all = static_cast<int64_t>(total) * a.pool.num_layers * a.pool.hk;
-    const int64_t per = (all + ra.ctas - 1) / ra.ctas;
+    const uint32_t all = total * a.pool.num_layers * a.pool.hk;
+    const uint32_t per = (all + ra.ctas - 1) / ra.ctas;
     run_lo = min(all, blockIdx.x * per);
     run_hi = min(all, run_lo + per);
   } else {
@@ -200,11 +213,11 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? 2 : 1)
   pdl::launch_dependents();
 
   // Entry of the list at place r of a (layer, head)'s work.
-  auto entry_at = [&](int32_t r) {
+  auto entry_at = [&](uint32_t r) {
     int32_t lo = 0, hi = kept;
     while (hi - lo > 1) {  // the last that starts at or before r
       const int32_t mid = (lo + hi) >> 1;
-      if (s_prefix[mid] <= r)
+      if (static_cast<uint32_t>(s_prefix[mid]) <= r)
         lo = mid;
       else
         hi = mid;
@@ -224,14 +237,14 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? 2 : 1)
       int64_t tok;
       float ks, vs;
     };
-    auto look = [&](int64_t w0) {
+    auto look = [&](uint32_t w0) {
       Look k{false, -1, 0, 0.f, 1.f};
-      const int64_t w = w0 + (lane >> 2);
+      const uint32_t w = w0 + (lane >> 2);
       if (w >= run_hi) return k;
-      const int64_t lh = w / max(total, 1);
-      const int32_t r = static_cast<int32_t>(w - lh * total);
+      const uint32_t lh = w / total;
+      const uint32_t r = w - lh * total;
       const int32_t e = entry_at(r);
-      const int32_t tile = r - s_prefix[e] - kLead;
+      const int32_t tile = static_cast<int32_t>(r) - s_prefix[e] - kLead;
       if (tile < 0) return k;
       k.tile = true;
       k.tok = static_cast<int64_t>(tile) * kTile + 16 * g;
@@ -242,8 +255,7 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? 2 : 1)
         problems |= CMR_DEVICE_CACHE_RANGE;
         return k;
       }
-      const int l = static_cast<int>((lh + lh0) / a.pool.hk);
-      const int h = static_cast<int>((lh + lh0) - static_cast<int64_t>(l) * a.pool.hk);
+      const uint32_t l = (lh + lh0) / a.pool.hk, h = lh + lh0 - l * a.pool.hk;
       k.unit = (static_cast<int64_t>(l) * a.pool.num_pages + id) * a.pool.hk + h;
       k.ks = __ldg(a.pool.ks + k.unit);
       k.vs = __ldg(a.pool.vs + k.unit);
@@ -252,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? 2 : 1)
     int stage = 0, phase = 0, issued = 0;
     bool dead = false;
     Look now = look(run_lo);
-    for (int64_t w = run_lo; w < run_hi && !dead; w += 8) {
+    for (uint32_t w = run_lo; w < run_hi && !dead; w += 8) {
       const uint32_t tiles = __ballot_sync(~0u, now.tile);
       const uint32_t pages = __ballot_sync(~0u, now.unit >= 0);
       for (int i = 0; i < 8; ++i) {
@@ -315,21 +327,20 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? 2 : 1)
   constexpr int H = D / (32 * VW);
 
   struct Segment {
-    int64_t w;        // its first place
-    int64_t lh;
+    uint32_t w;       // where the next begins
+    uint32_t lh;
     int32_t entry;
     int32_t t0, nt;   // tiles
     bool whole, late; // the whole item; the item started before this run
   };
   // The first segment at or behind place w; nt = 0 behind the last.
-  auto segment = [&](int64_t w) {
+  auto segment = [&](uint32_t w) {
     Segment sg{w, 0, 0, 0, 0, false, false};
     while (sg.w < run_hi) {
-      const int64_t lh = sg.w / total;
-      const int32_t r = static_cast<int32_t>(sg.w - lh * total);
-      const int32_t e = entry_at(r);
-      const int64_t start = lh * total + s_prefix[e], end = lh * total + s_prefix[e + 1];
-      const int64_t lo = max(sg.w, start + kLead), hi = min(end, run_hi);
+      const uint32_t lh = sg.w / total;
+      const int32_t e = entry_at(sg.w - lh * total);
+      const uint32_t start = lh * total + s_prefix[e], end = lh * total + s_prefix[e + 1];
+      const uint32_t lo = max(sg.w, start + kLead), hi = min(end, run_hi);
       if (lo < hi) {
         sg.lh = lh + lh0;
         sg.entry = e;
@@ -337,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? 2 : 1)
         sg.nt = static_cast<int32_t>(hi - lo);
         sg.whole = sg.t0 == 0 && hi == end;
         sg.late = start < run_lo;
-        sg.w = hi;  // where the next begins
+        sg.w = hi;
         return sg;
       }
       sg.w = min(end, run_hi);
@@ -372,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? 2 : 1)
   uint4 xq[kHave];
   if (sg.nt > 0) {
     l = static_cast<int>(sg.lh / a.pool.hk);
-    h = static_cast<int>(sg.lh - static_cast<int64_t>(l) * a.pool.hk);
+    h = static_cast<int>(sg.lh) - l * a.pool.hk;
     it = find_item<R>(a, first + sg.entry, &ignored);
     load_q(it, l, h, xq);
   }
@@ -432,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? 2 : 1)
     int next_l = 0, next_h = 0;
     if (next.nt > 0) {
       next_l = static_cast<int>(next.lh / a.pool.hk);
-      next_h = static_cast<int>(next.lh - static_cast<int64_t>(next_l) * a.pool.hk);
+      next_h = static_cast<int>(next.lh) - next_l * a.pool.hk;
       next_it = find_item<R>(a, first + next.entry, &ignored);
       load_q(next_it, next_l, next_h, xq);
     }
@@ -764,10 +775,9 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? 2 : 1)
       }
     }
     if (!sg.whole && sg.t0 == 0) {  // the run's last: it goes on in the next
-      const int64_t end = (sg.lh - lh0) * total + s_prefix[sg.entry + 1];
+      const uint32_t end = (sg.lh - lh0) * total + s_prefix[sg.entry + 1];
       left = make_int4(static_cast<int>(sg.lh), sg.entry,
-                       static_cast<int>((end - 1) / max(run_hi - run_lo, static_cast<int64_t>(1))),
-                       sg.late ? 0 : 1);
+                       static_cast<int>((end - 1) / max(run_hi - run_lo, 1u)), sg.late ? 0 : 1);
     }
     // the stage goes back: plain accesses before the next copy into it
     tma::fence_async_shared();
@@ -803,24 +813,24 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const RowsArg
   const int tid = threadIdx.x;
   const int32_t NB = ra.items;
   const int32_t bi = static_cast<int32_t>(blockIdx.x % NB);
-  const int64_t lh = blockIdx.x / NB;
+  const uint32_t lh = blockIdx.x / NB;
   bool bad = false;
   const Item it = find_item<R>(a, bi, &bad);  // of the call's inputs: no need to wait
   const int r = blockIdx.y;
   if (r >= it.rows) return;
   pdl::wait();
-  const int64_t total = __ldcg(ra.prefix + NB);
-  const int64_t start = lh * total + __ldcg(ra.prefix + bi);
-  const int64_t end = lh * total + __ldcg(ra.prefix + bi + 1);
-  const int64_t all = total * a.pool.num_layers * a.pool.hk;
-  const int64_t per = (all + ra.ctas - 1) / ra.ctas;
-  const int64_t c0 = (start + kLead) / per, c1 = (end - 1) / per;
+  const uint32_t total = __ldcg(ra.prefix + NB);
+  const uint32_t start = lh * total + __ldcg(ra.prefix + bi);
+  const uint32_t end = lh * total + __ldcg(ra.prefix + bi + 1);
+  const uint32_t all = total * a.pool.num_layers * a.pool.hk;
+  const uint32_t per = (all + ra.ctas - 1) / ra.ctas;
+  const uint32_t c0 = (start + kLead) / per, c1 = (end - 1) / per;
   if (c0 == c1) return;  // written whole
   const int n = static_cast<int>(c1 - c0 + 1);
   constexpr int kRec = R * (D + 2);
   auto record = [&](int k) {  // in the second place where the item starts within the run
-    const int64_t c = c0 + k;
-    return ra.partial + (c * 2 + (start >= c * per ? 1 : 0)) * kRec;
+    const uint32_t c = c0 + k;
+    return ra.partial + (static_cast<int64_t>(c) * 2 + (start >= c * per ? 1 : 0)) * kRec;
   };
   const int ln = tid % kJoinLanes, gr = tid / kJoinLanes;
   const int d = blockIdx.z * 4 * kJoinLanes + 4 * ln;
@@ -884,7 +894,7 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const RowsArg
     }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     const int l = static_cast<int>(lh / a.pool.hk);
-    const int h = static_cast<int>(lh - static_cast<int64_t>(l) * a.pool.hk);
+    const int h = static_cast<int>(lh) - l * a.pool.hk;
     const int f = it.first_row + r;
     uint16_t* dst = a.out + ((l * a.batch.n_tokens + it.tok + f / a.group) * a.hq + h * a.group +
                              f % a.group) * D + d;
@@ -1010,17 +1020,16 @@ cudaError_t launch_attend_rows(const AttendArgs& a, cudaStream_t stream) {
   ra.items = static_cast<int32_t>(nb);
   const int64_t cap = static_cast<int64_t>(a.table.max_pages) << a.pool.page_shift;
   const int64_t most_tiles = ((cap + kTile - 1) / kTile + kLead) * nb;  // per layer and head
-  if (nb <= kMaxSplitItems && most_tiles <= INT32_MAX) {
+  const int64_t lh = static_cast<int64_t>(a.pool.num_layers) * a.pool.hk;
+  if (nb <= kMaxSplitItems && most_tiles <= INT32_MAX / lh) {
     ra.prefix = static_cast<int32_t*>(a.workspace);
     ra.left = reinterpret_cast<int4*>(static_cast<uint8_t*>(a.workspace) +
                                       align16((nb + 1) * sizeof(int32_t)));
     ra.partial = reinterpret_cast<float*>(ra.left + max_ctas(R));
     // no more CTAs than there can be tiles
-    const int64_t tiles = most_tiles * a.pool.num_layers * a.pool.hk;
+    const int64_t tiles = most_tiles * lh;
     const int most = max_ctas(R);
     ra.ctas = tiles < most ? static_cast<int32_t>(tiles) : most;
-    // the joining grid has a block for every item and row
-    if (nb * a.pool.num_layers * a.pool.hk > INT32_MAX) return cudaErrorInvalidValue;
   }
   CUtensorMap k, v;
   if (!encode_pool_maps(a.pool, 16, &k, &v)) return cudaErrorNotSupported;

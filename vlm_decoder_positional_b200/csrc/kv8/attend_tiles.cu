@@ -136,6 +136,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t v_clean = s_full + 56;
 
   if (warp == 1) tc::alloc(tma::smem_addr(s_tmem), kColumns);
+  if (tid == 0) {
+    tma::prefetch_map(&k_map);
+    tma::prefetch_map(&v_map);
+  }
   // ---- the item: heavy (late) row tiles first
   const int32_t bi = ta.items - 1 - static_cast<int32_t>(blockIdx.x);
   const int64_t lh = blockIdx.y;

@@ -14,7 +14,9 @@ row of page_table, int32 [rows, max_pages], lists one sequence's pages in order
 page (0: free).
 """
 import ctypes
+import functools
 import os
+import struct
 from typing import Optional, Sequence, Tuple
 
 import torch
@@ -34,6 +36,13 @@ HEAD_DIMS = (64, 128, 256)
 _p, _i, _l, _d, _z = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_double,
                       ctypes.c_size_t)
 _POOL = [_p, _p, _p, _p]
+
+# cmr_kv8_call's numbers, and the packing of their words: the arguments in one array cost
+# half of what ctypes takes for each of them
+_CALLS = {"cmr_kv8_rotate_qk": (0, struct.Struct("=13qd14q")),
+          "cmr_kv8_attend": (1, struct.Struct("=10qd14q")),
+          "cmr_kv8_extend": (2, struct.Struct("=13q")), "cmr_kv8_fork": (3, struct.Struct("=21q")),
+          "cmr_kv8_free": (4, struct.Struct("=9q")), "cmr_kv8_compact": (5, struct.Struct("=17q"))}
 # name -> (restype, argtypes); mirrors include/cmr_kv8.h
 SIGNATURES = {
     "cmr_kv8_rotate_qk": (ctypes.c_int, [_p, _p, _p, _p, _i, _p, _p, _p, _l, _i, _i, _i, _i, _d,
@@ -49,6 +58,7 @@ SIGNATURES = {
     "cmr_kv8_compact": (ctypes.c_int, _POOL + [_i, _i, _i, _i, _i, _p, _i, _i, _p, _p, _z, _p,
                                                _p]),
     "cmr_kv8_pages_workspace_bytes": (_z, [_i, _i, _i]),
+    "cmr_kv8_call": (ctypes.c_int, [_i, ctypes.c_char_p, _i]),
     "cmr_kv8_last_attend_kernel": (ctypes.c_char_p, []),
     "cmr_kv8_last_error_message": (ctypes.c_char_p, []),
 }
@@ -114,11 +124,11 @@ def _ptr(t, name: str, dtype: torch.dtype, dev: torch.device, shape: Tuple[int, 
 
 
 def _maybe(t, name, dtype, dev, shape):
-    return None if t is None else _ptr(t, name, dtype, dev, shape)
+    return 0 if t is None else _ptr(t, name, dtype, dev, shape)
 
 
 def _status(t, dev):
-    return None if t is None else _want(t, "device_status", torch.int32, dev)
+    return 0 if t is None else _want(t, "device_status", torch.int32, dev)
 
 
 def _pool(k_pages, v_pages, k_scales, v_scales, dev):
@@ -135,13 +145,13 @@ def _pool(k_pages, v_pages, k_scales, v_scales, dev):
 def _heads(t, name, dev, n=None, L=None, D=None):
     """(pointer, (L, N, H, D)) of bf16 [L, N, H, D] or [N, H, D]."""
     p = _want(t, name, torch.bfloat16, dev)
-    s = tuple(t.shape)
-    s = (1,) + s if len(s) == 3 else s
+    s = t.shape
+    if len(s) == 3:
+        s = (1, *s)
     if len(s) != 4:
         raise ValueError(f"{name} must be [L, N, H, D] or [N, H, D]")
-    if (n is not None and s[1] != n) or (L is not None and s[0] != L) or \
-            (D is not None and s[3] != D):
-        raise ValueError(f"{name} shape {s} does not match L={L}, N={n}, D={D}")
+    if n is not None and (s[1] != n or s[0] != L or s[3] != D):
+        raise ValueError(f"{name} shape {tuple(s)} does not match L={L}, N={n}, D={D}")
     return p, s
 
 
@@ -157,7 +167,7 @@ def _table(page_table, dev):
 def _batch(cu_seqlens, pos_offset, slot, n, dev):
     """(num_seqs, pointers of cu_seqlens, pos_offset and slot)."""
     if cu_seqlens is None:
-        b, cu = n, None
+        b, cu = n, 0
     else:
         cu = _want(cu_seqlens, "cu_seqlens", torch.int32, dev)
         b = cu_seqlens.numel() - 1
@@ -182,14 +192,26 @@ def _workspace(workspace, need, dev, stream):
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
-def _call(name: str, dev: torch.device, args):
-    """The C function, with dev as the current device."""
-    f = getattr(_lib or lib(), name)
+@functools.lru_cache(maxsize=64)
+def _sections(t, h, w):
+    """(array, address) of the three counts."""
+    a = (_i * 3)(t, h, w)
+    return a, ctypes.addressof(a)
+
+
+def _call(name: str, dev: torch.device, *args):
+    """The C function on dev, as the current device; None stands for a null pointer."""
+    number, words = _CALLS[name]
+    try:
+        packed = words.pack(*args)
+    except struct.error as e:
+        raise TypeError(f"{name}: an argument is not a number of its kind ({e})") from None
+    f = (_lib or lib()).cmr_kv8_call
     if torch.cuda.current_device() == dev.index:
-        status = f(*args)
+        status = f(number, packed, len(packed) // 8)
     else:
         with torch.cuda.device(dev):
-            status = f(*args)
+            status = f(number, packed, len(packed) // 8)
     if status != CMR_OK:
         raise Kv8Error(status, name)
 
@@ -211,7 +233,7 @@ def rotate_qk_kv8(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor,
     L, n, hk, D = shape
     dev = k.device
     vp = _ptr(v, "v", torch.bfloat16, dev, k.shape)
-    qp, hq = None, 0
+    qp, hq = 0, 0
     if q is not None:
         qp, qs = _heads(q, "q", dev, n, L, D)
         hq = qs[2]
@@ -224,21 +246,26 @@ def rotate_qk_kv8(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor,
     ap = _ptr(amount, "amount", torch.int32, dev, (b,))
     st = _status(device_status, dev)
     if n and L:
-        _call("cmr_kv8_rotate_qk", dev, (
-            qp if hq else None, kp, vp, cu, b, off, sp, ap, n, L, hq, hk, D, theta,
-            (_i * 3)(*sections), rot_dim, *pool, pages, P, table, rows, cols, sl, st,
-            _raw_stream(dev, stream)))
+        _call("cmr_kv8_rotate_qk", dev, qp if hq else 0, kp, vp, cu, b, off, sp, ap, n, L, hq, hk, D,
+              theta, _sections(*sections)[1], rot_dim, *pool, pages, P, table, rows, cols, sl, st,
+              _raw_stream(dev, stream))
     return q
+
+
+@functools.lru_cache(maxsize=1024)
+def _attend_bytes(index, *sizes):
+    with torch.cuda.device(index):
+        return lib().cmr_kv8_attend_workspace_bytes(*sizes)
 
 
 def attend_kv8_workspace_bytes(num_seqs: int, n_tokens: int, num_layers: int, hq: int, hk: int,
                                head_dim: int, device: Optional[torch.device] = None) -> int:
     """Workspace bytes of attend_kv8 for these sizes on a device (default: the current)."""
-    f = lib().cmr_kv8_attend_workspace_bytes
-    if device is None or device.index in (None, torch.cuda.current_device()):
-        return f(num_seqs, n_tokens, num_layers, hq, hk, head_dim)
-    with torch.cuda.device(device):
-        return f(num_seqs, n_tokens, num_layers, hq, hk, head_dim)
+    index = None if device is None else torch.device(device).index
+    if not torch.cuda.is_available():  # sizes that leave nothing to do need no device
+        return lib().cmr_kv8_attend_workspace_bytes(num_seqs, n_tokens, num_layers, hq, hk, head_dim)
+    return _attend_bytes(torch.cuda.current_device() if index is None else index, num_seqs,
+                         n_tokens, num_layers, hq, hk, head_dim)
 
 
 def attend_kv8(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
@@ -269,11 +296,11 @@ def attend_kv8(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
     op = _ptr(out, "out", torch.bfloat16, dev, q.shape)
     st = _status(device_status, dev)
     if n and L:
-        ws, wp, wb = _workspace(workspace, attend_kv8_workspace_bytes(b, n, L, hq, hk, D, dev)
+        ws, wp, wb = _workspace(workspace, _attend_bytes(dev.index, b, n, L, hq, hk, D)
                                 if workspace is None else 0, dev, stream)
-        _call("cmr_kv8_attend", dev, (
-            qp, op, cu, b, off, n, L, hq, hk, D, D ** -0.5 if scale is None else scale, *pool,
-            pages, P, table, rows, cols, sl, wp, wb, st, _raw_stream(dev, stream)))
+        _call("cmr_kv8_attend", dev, qp, op, cu, b, off, n, L, hq, hk, D,
+              D ** -0.5 if scale is None else scale, *pool, pages, P, table, rows, cols, sl, wp,
+              wb, st, _raw_stream(dev, stream))
     return out
 
 
@@ -282,9 +309,10 @@ def last_attend_kernel() -> str:
     return lib().cmr_kv8_last_attend_kernel().decode()
 
 
+@functools.lru_cache(maxsize=1024)
 def kv8_pages_workspace_bytes(table_rows: int, num_pages: int, n: int = 0) -> int:
     """Workspace bytes of the page calls for a table, a pool and n entries."""
-    return int(lib().cmr_kv8_pages_workspace_bytes(int(table_rows), int(num_pages), int(n)))
+    return lib().cmr_kv8_pages_workspace_bytes(table_rows, num_pages, n)
 
 
 def _pages_state(page_table, page_refs, pages=None):
@@ -299,7 +327,7 @@ def _pages_call(name, dev, before, after, rows, pages, n, workspace, device_stat
     st = _status(device_status, dev)
     ws, wp, wb = _workspace(workspace, kv8_pages_workspace_bytes(rows, pages, n)
                             if workspace is None else 0, dev, stream)
-    _call(name, dev, (*before, *after, wp, wb, st, _raw_stream(dev, stream)))
+    _call(name, dev, *before, *after, wp, wb, st, _raw_stream(dev, stream))
 
 
 def kv8_extend(page_table: torch.Tensor, page_refs: torch.Tensor, slots: torch.Tensor,
@@ -348,8 +376,8 @@ def kv8_free(page_table: torch.Tensor, page_refs: torch.Tensor, slots: torch.Ten
     n = slots.numel()
     s = _ptr(slots, "slots", torch.int32, dev, (n,))
     if n:
-        _call("cmr_kv8_free", dev, (t, rows, cols, r, pages, s, n, _status(device_status, dev),
-                                    _raw_stream(dev, stream)))
+        _call("cmr_kv8_free", dev, t, rows, cols, r, pages, s, n, _status(device_status, dev),
+              _raw_stream(dev, stream))
     return page_table
 
 
