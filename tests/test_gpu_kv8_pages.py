@@ -199,6 +199,84 @@ def test_captured_and_replayed(cuda_device):
     assert not b.refs.any() and (b.c.table == -1).all()
 
 
+def test_calls_follow_what_other_streams_and_libraries_enqueue(cuda_device):
+    """Each call's first kernel may be placed before the work ahead of it ends, but must
+    see all of it: long kernels of torch write every input just before, on the same
+    stream, on another one behind an event, and inside a capture with such a join."""
+    dev = cuda_device
+    L, B, D, P = 1, 4, 64, 16
+    g = torch.Generator(device=dev).manual_seed(0)
+    rand = lambda *s: torch.randn(s, generator=g, device=dev).to(torch.bfloat16)
+    b = Both(dev, B, 8, 40, P=P, L=L, hk=2, D=D)
+    src = [rand(L, B, h, D) for h in (4, 2, 2)]
+    off0, lens0 = i32([5, 30, 77, 0], dev), i32([6, 31, 78, 1], dev)
+    slots = i32([0, 1, 2, 3], dev)
+    start, amount = i32([cmr.TEXT_ONLY_START] * B, dev), i32([0] * B, dev)
+    big = torch.ones(1 << 27, device=dev)
+    held = [b.c.table, b.refs, b.c.ks, b.c.vs, b.c.k.view(torch.uint8), b.c.v.view(torch.uint8)]
+    state = [x.clone() for x in held]
+
+    def work(inputs, out):
+        q, k, v, off, lens = inputs
+        big.mul_(1.0)                                  # half a GB twice: about 0.2 ms
+        for x, y in zip((q, k, v, off, lens), (*src, off0, lens0)):
+            x.copy_(y)
+        return q, k, v, off, lens
+
+    def calls(inputs, out, side=None):
+        if side is None:
+            work(inputs, out)
+        else:
+            cur = torch.cuda.current_stream()
+            side.wait_stream(cur)
+            with torch.cuda.stream(side):
+                work(inputs, out)
+            cur.wait_stream(side)
+        q, k, v, off, lens = inputs
+        pkg.kv8_extend(b.c.table, b.refs, slots, lens, P)
+        pkg.rotate_qk_kv8(q, k, v, start, amount, *b.c.pool(), b.c.table, pos_offset=off)
+        pkg.attend_kv8(q, *b.c.pool(), b.c.table, pos_offset=off, out=out)
+        pkg.kv8_free(b.c.table, b.refs, slots)
+        pkg.kv8_compact(*b.c.pool(), b.c.table, b.refs)
+
+    def fresh():
+        return [torch.zeros_like(x) for x in (*src, off0, lens0)], torch.zeros_like(src[0])
+
+    def reset():
+        for x, y in zip(held, state):
+            x.copy_(y)
+        torch.cuda.synchronize()
+
+    reset()
+    inputs, want = fresh()
+    calls(inputs, want)
+    torch.cuda.synchronize()
+    assert want.abs().sum() > 0 and not b.refs.any()
+    side = torch.cuda.Stream()
+    for other in (None, side):
+        for _ in range(4):
+            reset()
+            inputs, out = fresh()
+            torch.cuda.synchronize()
+            calls(inputs, out, other)
+            torch.cuda.synchronize()
+            assert torch.equal(out, want)
+    inputs, out = fresh()
+    main = torch.cuda.Stream()
+    main.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=main):
+        calls(inputs, out, side)
+    for _ in range(3):
+        reset()
+        for x in (*inputs, out):
+            x.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+
+
 def test_a_serving_loop(cuda_device):
     """Prompts in, branches forked, tokens appended to each, some sequences leave, the pool
     is compacted, others come: at each point the attention equals the model's over the

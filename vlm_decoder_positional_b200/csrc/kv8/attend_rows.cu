@@ -149,6 +149,7 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? 2 : 1)
     }
     tma::mbar_init_fence();
   }
+  pdl::wait();
   // What the first copies will wait for, one after another, is asked for at once: the
   // tensor maps, and the page table, a line to a thread of the grid.
   if (tid == 32) {
@@ -817,8 +818,9 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const RowsArg
   bool bad = false;
   const Item it = find_item<R>(a, bi, &bad);  // of the call's inputs: no need to wait
   const int r = blockIdx.y;
-  if (r >= it.rows) return;
   pdl::wait();
+  pdl::launch_dependents();
+  if (r >= it.rows) return;
   const uint32_t total = __ldcg(ra.prefix + NB);
   const uint32_t start = lh * total + __ldcg(ra.prefix + bi);
   const uint32_t end = lh * total + __ldcg(ra.prefix + bi + 1);
@@ -911,6 +913,7 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_runs_kernel(const Ro
   constexpr int kRec = R * (D + 2);
   const AttendArgs& a = ra.a;
   pdl::wait();
+  pdl::launch_dependents();
   const int4 left = __ldcg(ra.left + blockIdx.x);
   if (left.x < 0) return;
   const int64_t lh = left.x;
@@ -972,11 +975,11 @@ cudaError_t launch(const RowsArgs& ra, const CUtensorMap& k, const CUtensorMap& 
   if (e != cudaSuccess) return e;
   if (ra.ctas == 0) {
     if (lh > 65535) return cudaErrorInvalidValue;
-    attend_rows_kernel<D, NQ><<<dim3(ra.items, static_cast<unsigned>(lh)), kThreads, smem, stream>>>(ra, k, v);
-    return cudaGetLastError();
+    return pdl::launch(attend_rows_kernel<D, NQ>, dim3(ra.items, static_cast<unsigned>(lh)),
+                       dim3(kThreads), smem, stream, true, ra, k, v);
   }
-  attend_rows_kernel<D, NQ><<<ra.ctas, kThreads, smem, stream>>>(ra, k, v);
-  e = cudaGetLastError();
+  e = pdl::launch(attend_rows_kernel<D, NQ>, dim3(ra.ctas), dim3(kThreads), smem, stream, true, ra,
+                  k, v);
   if (e != cudaSuccess || ra.ctas == 1) return e;
   // With one item to four runs or more, an item is cut into a few pieces: a CTA
   // joins them all.  With fewer items there are many pieces, and the CTAs share

@@ -140,6 +140,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma::prefetch_map(&k_map);
     tma::prefetch_map(&v_map);
   }
+  pdl::wait();
   // ---- the item: heavy (late) row tiles first
   const int32_t bi = ta.items - 1 - static_cast<int32_t>(blockIdx.x);
   const int64_t lh = blockIdx.y;
@@ -679,6 +680,7 @@ template <int D>
 __global__ void __launch_bounds__(kJoinThreads) attend_tiles_join_kernel(const TilesArgs ta) {
   const AttendArgs& a = ta.a;
   pdl::wait();
+  pdl::launch_dependents();
   const int32_t bi = static_cast<int32_t>(blockIdx.x % ta.items);
   const int64_t lh = blockIdx.x / ta.items;
   bool bad = false;
@@ -732,9 +734,8 @@ cudaError_t launch(const TilesArgs& ta, const CUtensorMap& k, const CUtensorMap&
   cudaError_t e = cudaFuncSetAttribute(attend_tiles_kernel<D>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
   if (e != cudaSuccess) return e;
-  attend_tiles_kernel<D><<<dim3(ta.items, static_cast<unsigned>(lh), ta.splits), kThreads,
-                           S::kBytes, stream>>>(ta, k, v);
-  e = cudaGetLastError();
+  e = pdl::launch(attend_tiles_kernel<D>, dim3(ta.items, static_cast<unsigned>(lh), ta.splits),
+                  dim3(kThreads), S::kBytes, stream, true, ta, k, v);
   if (e != cudaSuccess || ta.splits == 1) return e;
   constexpr int kPer = kJoinThreads / (D / 4);
   return pdl::launch(attend_tiles_join_kernel<D>,

@@ -8,6 +8,12 @@
 #include "../cmr_internal.cuh"
 #include "cmr_kv8.h"
 
+// All kernels here are launched with programmatic stream serialization: their CTAs
+// may be placed while the kernel before them in the stream drains.  Every CTA of
+// every one of them waits (pdl::wait) before it touches memory that another kernel
+// could have written, whoever launched that kernel, so a launch never sees unfinished
+// work; what overlaps is the launch itself, which took 2 of the 58 us of a decode
+// step's attention (64 x 4,096 tokens).
 namespace cmr {
 namespace kv8 {
 

@@ -117,6 +117,8 @@ __device__ __forceinline__ int64_t pages_for(int32_t tokens, int32_t page_tokens
 }
 
 __global__ void __launch_bounds__(kPlanThreads) extend_kernel(const PagesArgs a) {
+  pdl::wait();
+  pdl::launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
   int32_t* need = a.workspace + kHead;  // [n]
   int32_t* have = need + a.n;           // [n]
@@ -180,6 +182,7 @@ __global__ void __launch_bounds__(kPlanThreads) extend_kernel(const PagesArgs a)
 // Which entries of a fork hold, their shared pages and their own last page; the
 // copies are left as jobs (from, to, rows) in the workspace.
 __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const PagesArgs a) {
+  pdl::wait();
   pdl::launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
   const int P = a.page_tokens;
@@ -273,6 +276,7 @@ __device__ __forceinline__ void copy_chunks(uint4* dst, const uint4* src, int n1
 // time, and its scale.
 __global__ void __launch_bounds__(kCopyThreads) fork_copy_kernel(const PagesArgs a) {
   pdl::wait();
+  pdl::launch_dependents();
   const int32_t* jobs = a.workspace + kHead;
   const int hk = a.pool.hk, D = a.pool.head_dim;
   const int64_t page = static_cast<int64_t>(a.page_tokens) * D;
@@ -296,6 +300,8 @@ __global__ void __launch_bounds__(kCopyThreads) fork_copy_kernel(const PagesArgs
 
 // A CTA per named row.
 __global__ void __launch_bounds__(kFreeThreads) free_kernel(const PagesArgs a) {
+  pdl::wait();
+  pdl::launch_dependents();
   __shared__ int s_end;
   const int i = blockIdx.x;
   const int32_t slot = __ldg(a.dst + i);
@@ -329,6 +335,7 @@ __global__ void __launch_bounds__(kFreeThreads) free_kernel(const PagesArgs a) {
 }
 
 __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const PagesArgs a) {
+  pdl::wait();
   pdl::launch_dependents();
   int32_t* to = a.workspace + kHead;
   int32_t* from = to + a.pool.num_pages;
@@ -349,6 +356,7 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const PagesA
 // renames them in the table.
 __global__ void __launch_bounds__(kCopyThreads) compact_move_kernel(const PagesArgs a) {
   pdl::wait();
+  pdl::launch_dependents();
   const int32_t* to = a.workspace + kHead;
   const int32_t* from = to + a.pool.num_pages;
   const int moves = __ldcg(a.workspace + kJobs);
@@ -403,26 +411,24 @@ size_t pages_workspace_bytes(int32_t rows, int32_t num_pages, int32_t n) {
 }
 
 cudaError_t launch_extend(const PagesArgs& a, cudaStream_t stream) {
-  extend_kernel<<<1, kPlanThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  return pdl::launch(extend_kernel, dim3(1), dim3(kPlanThreads), 0, stream, true, a);
 }
 
 cudaError_t launch_fork(const PagesArgs& a, cudaStream_t stream) {
-  fork_plan_kernel<<<1, kPlanThreads, 0, stream>>>(a);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e =
+      pdl::launch(fork_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, true, a);
   if (e != cudaSuccess) return e;
   const int64_t units = static_cast<int64_t>(a.n) * a.pool.num_layers * a.pool.hk * 2;
   return pdl::launch(fork_copy_kernel, dim3(copy_grid(units)), dim3(kCopyThreads), 0, stream, true, a);
 }
 
 cudaError_t launch_free(const PagesArgs& a, cudaStream_t stream) {
-  free_kernel<<<a.n, kFreeThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  return pdl::launch(free_kernel, dim3(a.n), dim3(kFreeThreads), 0, stream, true, a);
 }
 
 cudaError_t launch_compact(const PagesArgs& a, cudaStream_t stream) {
-  compact_plan_kernel<<<1, kPlanThreads, 0, stream>>>(a);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e =
+      pdl::launch(compact_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, true, a);
   if (e != cudaSuccess) return e;
   const int64_t units = static_cast<int64_t>(a.pool.num_pages / 2 + 1) * a.pool.num_layers * 2;
   return pdl::launch(compact_move_kernel, dim3(copy_grid(units)), dim3(kCopyThreads), 0, stream, true, a);

@@ -25,6 +25,7 @@
 #include <mutex>
 
 #include "kv8.cuh"
+#include "../pdl.cuh"
 #include "../rotate_common.cuh"
 
 namespace cmr {
@@ -411,6 +412,8 @@ __global__ void __launch_bounds__(kThreads, P * D <= 64 * 256 ? 3 : 2)
     s_plane[j] = table.plane[j];
   }
   __syncthreads();
+  pdl::wait();
+  pdl::launch_dependents();
 
   const int64_t kv_blocks = static_cast<int64_t>(units) * groups;
   if (blockIdx.x >= kv_blocks) {
@@ -491,6 +494,8 @@ __global__ void __launch_bounds__(kStepThreads)
     write_step_kernel(const WriteArgs a, const FreqTable table) {
   constexpr int D8 = D / 8;
   __shared__ float2 s_cs[kStepWarps][kMaxFreqs];
+  pdl::wait();
+  pdl::launch_dependents();
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
   const int F = a.rot_dim / 2, U = F / 8;
   const int64_t item = static_cast<int64_t>(blockIdx.x) * kStepWarps + warp;
@@ -602,9 +607,9 @@ cudaError_t launch_pages(const WriteArgs& a, const FreqTable& table, cudaStream_
   }
   const int64_t blocks = units * groups + q_blocks;
   if (units > INT32_MAX || blocks > INT32_MAX) return cudaErrorInvalidValue;
-  write_pages_kernel<D, P><<<static_cast<unsigned>(blocks), kThreads, smem, stream>>>(
-      a, table, static_cast<int32_t>(units), groups, per, q_groups, q_per);
-  return cudaGetLastError();
+  return pdl::launch(write_pages_kernel<D, P>, dim3(static_cast<unsigned>(blocks)), dim3(kThreads),
+                     smem, stream, true, a, table, static_cast<int32_t>(units), groups, per,
+                     q_groups, q_per);
 }
 
 template <int D>
@@ -623,8 +628,8 @@ cudaError_t launch_step(const WriteArgs& a, const FreqTable& table, cudaStream_t
   const int64_t items = B * L * a.pool.hk + (a.hq > 0 ? B * L : 0);
   const int64_t blocks = (items + kStepWarps - 1) / kStepWarps;
   if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-  write_step_kernel<D><<<static_cast<unsigned>(blocks), kStepThreads, 0, stream>>>(a, table);
-  return cudaGetLastError();
+  return pdl::launch(write_step_kernel<D>, dim3(static_cast<unsigned>(blocks)),
+                     dim3(kStepThreads), 0, stream, true, a, table);
 }
 
 }  // namespace
