@@ -71,7 +71,8 @@ extern "C" {
  *                     are skipped)
  * hq may be 0 (q NULL); hk >= 1.  q, k, v, k_pages and v_pages 16-byte aligned.
  * Errors: CMR_EINVAL for any violation above, CMR_EUNSUPPORTED for another
- * head_dim or page_tokens. */
+ * head_dim or page_tokens, hk * head_dim over 2^23, or num_layers * num_pages * hk or
+ * (hq + hk) * num_layers over INT32_MAX. */
 CMR_API cmr_status cmr_kv8_rotate_qk(void* q, const void* k, const void* v,
                                      const int32_t* cu_seqlens, int32_t num_seqs,
                                      const int32_t* pos_offset, const int32_t* start,
@@ -108,8 +109,13 @@ CMR_API cmr_status cmr_kv8_rotate_qk(void* q, const void* k, const void* v,
  *                     those indices were not there), CMR_DEVICE_BAD_CU_SEQLENS,
  *                     CMR_DEVICE_WAIT_TIMEOUT
  *   the rest          as in cmr_kv8_rotate_qk
- * Errors: CMR_EINVAL for any violation above, CMR_EUNSUPPORTED for another
- * head_dim or page_tokens. */
+ * Scores (scale * q . k) have to lie within fp32's range.
+ * Calls of one token per sequence, or of a few, run a kernel that shares each key and
+ * value among 8 or 16 rows and is bound by reading the cache; calls of more than 16
+ * rows (tokens x hq / hk) per sequence on average run one of 128 rows on the
+ * tensor cores.  A batch of both kinds is quicker as two calls.
+ * Errors: as cmr_kv8_rotate_qk, and CMR_EINVAL when max_pages * page_tokens is over
+ * INT32_MAX - 256. */
 CMR_API cmr_status cmr_kv8_attend(const void* q, void* out, const int32_t* cu_seqlens,
                                   int32_t num_seqs, const int32_t* pos_offset, int64_t n_tokens,
                                   int32_t num_layers, int32_t hq, int32_t hk, int32_t head_dim,

@@ -64,7 +64,8 @@ def call_write(lib, **kw):
     (dict(k=None), 1), (dict(v=None), 1), (dict(k=FAKE + 8), 1), (dict(q=FAKE + 2), 1),
     (dict(kp=None), 1), (dict(vp=FAKE + 4), 1), (dict(ks=None), 1), (dict(vs=FAKE + 2), 1),
     (dict(table=None), 1), (dict(start=None), 1), (dict(amount=None), 1), (dict(slot=FAKE + 1), 1),
-    (dict(cu=None, seqs=3), 1), (dict(hk=1 << 20, L=1 << 12), 3), (dict(), 1),
+    (dict(cu=None, seqs=3), 1), (dict(hk=1 << 20, L=1 << 12), 3), (dict(hk=1 << 16), 3),
+    (dict(pages=1 << 30, hk=4), 3), (dict(), 1),
 ])
 def test_write_rejects_bad_arguments_on_the_host(lib, kw, want):
     # the last case is well formed but for its addresses, which no device has

@@ -99,6 +99,10 @@ cmr_status check_pool(const void* k_pages, const void* v_pages, const float* k_s
     return fail(CMR_EUNSUPPORTED, "page_tokens must be 16, 32, 64 or 128, got %d", page_tokens);
   if (static_cast<int64_t>(hk) * num_layers > INT32_MAX)
     return fail(CMR_EUNSUPPORTED, "hk * num_layers exceeds INT32_MAX");
+  if (static_cast<int64_t>(hk) * num_layers > INT32_MAX / num_pages)
+    return fail(CMR_EUNSUPPORTED, "num_layers * num_pages * hk exceeds INT32_MAX");
+  if (hk > (1 << 23) / head_dim)
+    return fail(CMR_EUNSUPPORTED, "hk * head_dim exceeds 2^23");
   cmr_status s;
   if ((s = check(k_pages, "k_pages", 16)) != CMR_OK) return s;
   if ((s = check(v_pages, "v_pages", 16)) != CMR_OK) return s;
