@@ -61,16 +61,21 @@ __device__ int64_t block_scan(int v, int64_t* total) {
   return s_warp[warp] + x - v;
 }
 
+// This warp's share [s0, s1) of pages [lo, hi): equal segments of whole lines.
+__device__ __forceinline__ void warp_segment(int lo, int hi, int& s0, int& s1) {
+  const int64_t span = (static_cast<int64_t>(hi) - lo + kPlanWarps - 1) / kPlanWarps;
+  const int64_t seg = (span + 31) / 32 * 32, at = lo + (threadIdx.x / 32) * seg;
+  s0 = static_cast<int>(at < hi ? at : hi);
+  s1 = static_cast<int>(at + seg < hi ? at + seg : hi);
+}
+
 // Lists in `out`, lowest first, the pages of [lo, hi) that are free (or in use),
 // at most `limit` of them; returns how many there are in all.
 __device__ int select_pages(const int32_t* refs, int lo, int hi, bool want_free, int limit,
                             int32_t* out) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
-  const int64_t span = (static_cast<int64_t>(hi) - lo + kPlanWarps - 1) / kPlanWarps;
-  const int seg = static_cast<int>((span + 31) / 32 * 32);
-  const int64_t s64 = lo + static_cast<int64_t>(warp) * seg;
-  const int s0 = static_cast<int>(s64 < hi ? s64 : hi);
-  const int s1 = static_cast<int>(s64 + seg < hi ? s64 + seg : hi);
+  const int lane = threadIdx.x & 31;
+  int s0, s1;
+  warp_segment(lo, hi, s0, s1);
   int count = 0;
 #pragma unroll 8
   for (int i = s0 + lane; i < s1; i += 32) count += (__ldcg(refs + i) <= 0) == want_free;
@@ -98,18 +103,11 @@ __device__ bool named_before(const int32_t* slots, int i, int32_t slot) {
   return __any_sync(~0u, same);
 }
 
-// Pages of a row: its entries before the first negative one.
+// Pages of a row: its entries before the first negative one (asked by a whole warp).
 __device__ int row_pages(const PagesArgs& a, int32_t row) {
   const int32_t* r = a.table + static_cast<int64_t>(row) * a.max_pages;
-  int lo = 0, hi = a.max_pages;  // entries below lo are pages, those from hi on are not
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (__ldcg(r + mid) >= 0)
-      lo = mid + 1;
-    else
-      hi = mid;
-  }
-  return lo;
+  const int last = last_true(a.max_pages, [&](int32_t k) { return __ldcg(r + k) >= 0; });
+  return __ldcg(r + last) >= 0 ? last + 1 : 0;
 }
 
 __device__ __forceinline__ int64_t pages_for(int32_t tokens, int32_t page_tokens) {
@@ -127,12 +125,12 @@ __global__ void __launch_bounds__(kPlanThreads) extend_kernel(const PagesArgs a)
   for (int i = warp; i < a.n; i += kPlanWarps) {
     const int32_t slot = __ldg(a.dst + i), len = __ldg(a.lens + i);
     const bool known = slot >= 0 && slot < a.rows && !named_before(a.dst, i, slot);
+    const int held = known ? row_pages(a, slot) : 0;
     if (lane == 0) {
-      int more = 0, held = 0;
+      int more = 0;
       if (!known || len < 0) {
         flag(a, CMR_DEVICE_CACHE_RANGE);
       } else {
-        held = row_pages(a, slot);
         const int64_t want = pages_for(len, a.page_tokens);
         if (want > a.max_pages)
           flag(a, CMR_DEVICE_CACHE_RANGE);
@@ -335,13 +333,47 @@ __global__ void __launch_bounds__(kFreeThreads) free_kernel(const PagesArgs a) {
 }
 
 __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const PagesArgs a) {
+  __shared__ int s_below;  // pages in use among the first `live`
   pdl::wait();
   pdl::launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const int n = a.pool.num_pages;
   int32_t* to = a.workspace + kHead;
-  int32_t* from = to + a.pool.num_pages;
-  const int live = select_pages(a.refs, 0, a.pool.num_pages, false, 0, nullptr);
-  const int holes = select_pages(a.refs, 0, live, true, a.pool.num_pages, to);
-  select_pages(a.refs, live, a.pool.num_pages, false, a.pool.num_pages, from);
+  int32_t* from = to + n;
+  // pages in use, of each warp's segment and before it
+  int s0, s1;
+  warp_segment(0, n, s0, s1);
+  int used = 0;
+#pragma unroll 8
+  for (int i = s0 + lane; i < s1; i += 32) used += __ldcg(a.refs + i) > 0;
+  used = __reduce_add_sync(~0u, used);
+  int64_t sum;
+  int before = static_cast<int>(block_scan(lane == 0 ? used : 0, &sum));
+  before = __shfl_sync(~0u, before, 0);
+  const int live = static_cast<int>(sum);
+  // those below `live`: the segment that the border falls into counts up to it
+  if (live >= s0 && (live < s1 || (live == n && s1 == n && s0 < s1))) {
+    int below = 0;
+    for (int i = s0 + lane; i < min(s1, live); i += 32) below += __ldcg(a.refs + i) > 0;
+    below = __reduce_add_sync(~0u, below);
+    if (lane == 0) s_below = before + below;
+  }
+  __syncthreads();
+  // the free ones below the border and the used ones from it on, both in order
+  const int below = s_below;
+  int at = before;
+#pragma unroll 4
+  for (int i0 = s0; i0 < s1; i0 += 32) {
+    const int i = i0 + lane;
+    const bool in = i < s1, use = in && __ldcg(a.refs + i) > 0;
+    const uint32_t uses = __ballot_sync(~0u, use);
+    const int u = at + __popc(uses & ((1u << lane) - 1));  // used ones before page i
+    if (in && !use && i < live) to[i - u] = i;
+    if (use && i >= live) from[u - below] = i;
+    at += __popc(uses);
+  }
+  __syncthreads();
+  const int holes = live - below;
   for (int i = threadIdx.x; i < holes; i += kPlanThreads) {
     a.refs[to[i]] = a.refs[from[i]];
     a.refs[from[i]] = 0;
