@@ -248,6 +248,46 @@ def test_slow_memory_changes_nothing(cuda_device, lens, offs, D):
         assert torch.equal(out, want)
 
 
+def test_pages_beyond_four_gigabytes(cuda_device):
+    # codes whose byte offsets pass 32 bits: the last pages of a pool of 4.6 GB for K and as
+    # much for V, written and read by each kernel
+    dev = cuda_device
+    pages, P, D, hk = 35000, 128, 256, 2
+    c = Cache(dev, [1], 1, hk, D, 16)
+    c.P, c.pages = P, pages
+    c.k, c.v = (torch.empty((2, pages, hk, P, D), dtype=torch.uint8, device=dev)
+                .view(torch.float8_e4m3fn) for _ in range(2))
+    c.L = 2
+    c.ks, c.vs = (torch.ones((2, pages, hk), device=dev) for _ in range(2))
+    c.table = i32([[pages - 1, 3, pages - 2], [pages - 3, pages - 5, -1]], dev)
+    g = torch.Generator(device=dev).manual_seed(0)
+    rand = lambda *s: torch.randn(s, generator=g, device=dev).to(torch.bfloat16)
+    text = i32([1 << 30] * 2, dev), i32([0, 0], dev)
+    k, v = rand(2, 500, hk, D), rand(2, 500, hk, D)
+    pkg.rotate_qk_kv8(None, k, v, *text, *c.pool(), c.table, cu_seqlens=i32([0, 300, 500], dev))
+    run(dev, [300, 200], [0, 0], L=2, D=D, P=P, cache=c, kernel="attend_tiles_kernel")
+    pkg.rotate_qk_kv8(None, k[:, :2].contiguous(), v[:, :2].contiguous(), *text, *c.pool(), c.table,
+                      pos_offset=i32([300, 200], dev))
+    run(dev, [1, 1], [300, 200], L=2, D=D, P=P, cache=c, step=True, kernel="attend_rows_kernel")
+    refs = torch.zeros(pages, dtype=torch.int32, device=dev)
+    for p in c.table.flatten().tolist():
+        if p >= 0:
+            refs[p] = 1
+    want = [c.values(w, 1, r, 1, n).clone() for w in "kv" for r, n in ((0, 301), (1, 201))]
+    pkg.kv8_compact(*c.pool(), c.table, refs)
+    assert int(c.table.max()) == 4
+    got = [c.values(w, 1, r, 1, n) for w in "kv" for r, n in ((0, 301), (1, 201))]
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+def test_sequences_of_one_token_with_cu_seqlens_are_a_step(cuda_device):
+    offs = [300, 5, 64, 1000]
+    a, q, c = run(cuda_device, [1] * 4, offs, step=True)
+    b = pkg.attend_kv8(q, *c.pool(), c.table, cu_seqlens=i32([0, 1, 2, 3, 4], cuda_device),
+                       pos_offset=i32(offs, cuda_device))
+    assert torch.equal(a, b)
+
+
 def test_empty_calls(cuda_device):
     dev = cuda_device
     c = Cache(dev, [1])
