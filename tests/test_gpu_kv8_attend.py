@@ -87,6 +87,42 @@ def test_one_long_sequence(cuda_device):
     run(cuda_device, [40], [20000], hq=8, hk=2, D=128, P=16)
 
 
+@pytest.mark.parametrize("lens, offs, shape", [
+    ([1] * 33 + [130], [200] * 33 + [30000], dict(D=64)),
+    ([100] + [6] * 255, [9000] + [70] * 255, dict(D=64, hq=4)),
+    ([100] + [6] * 256, [9000] + [70] * 256, dict(D=64, hq=4)),
+    ([100] + [6] * 255, [9000] + [70] * 255, dict(D=64)),                    # as many as are planned
+    ([100] + [6] * 256, [9000] + [70] * 256, dict(D=64)),                    # one more
+    ([0, 40, 0, 0, 300, 7], [5, 4000, 70, 0, 0, 900], dict(L=5, hk=1, P=16)),  # 29 to a head
+    ([60, 20], [3000, 100], dict(L=37, hq=2, hk=2, D=64)),                   # 2 to a head
+    ([60, 20], [3000, 100], dict(L=38, hq=2, hk=2, D=64)),                   # 1: none is split
+    ([128], [127], dict(hq=1, hk=1, D=128)),                                 # a row tile of two tiles
+    ([2000], [0], dict(hq=2, hk=1, D=128))])
+def test_items_cut_in_pieces(cuda_device, lens, offs, shape):
+    # whatever the workspace holds before
+    L, D, hq, hk = (shape.get(k, d) for k, d in (("L", 1), ("D", 256), ("hq", 8), ("hk", 2)))
+    need = pkg.attend_kv8_workspace_bytes(len(lens), sum(lens), L, hq, hk, D)
+    kernel = "attend_tiles_kernel" if sum(lens) * hq // hk > 16 * len(lens) else "attend_rows_kernel"
+    for fill in (0x7F, 0xFF):
+        ws = torch.full((need,), fill, dtype=torch.uint8, device=cuda_device)
+        run(cuda_device, lens, offs, kernel=kernel, workspace=ws, **shape)
+
+
+def test_a_step_of_a_large_group_cut_in_pieces(cuda_device):
+    run(cuda_device, [1] * 3, [5, 9000, 300], hq=40, hk=1, D=128, step=True,
+        kernel="attend_tiles_kernel")
+
+
+def test_sequences_that_overlap_are_flagged(cuda_device):
+    dev = cuda_device
+    c = Cache(dev, [40] * 4)
+    cu, offs = i32([0, 200, 100, 300, 0], dev), i32([2000] * 4, dev)
+    q = torch.ones((1, 300, 8, 256), device=dev, dtype=torch.bfloat16)
+    status = torch.zeros(1, dtype=torch.int32, device=dev)
+    pkg.attend_kv8(q, *c.pool(), c.table, cu_seqlens=cu, pos_offset=offs, device_status=status)
+    assert int(status.item()) == 1
+
+
 def test_slots_and_rows_behind_the_last_sequence(cuda_device):
     run(cuda_device, [1, 1, 1], [40, 3, 200], slot=[5, 0, 3], step=True)
     run(cuda_device, [30, 1, 90], [40, 3, 0], slot=[1, 4, 0], tail=37)

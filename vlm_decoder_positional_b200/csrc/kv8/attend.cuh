@@ -15,8 +15,7 @@ cudaError_t launch_attend_rows(const AttendArgs& a, cudaStream_t stream);
 
 // The tcgen05 kernel for many rows (attend_tiles.cu): *launched false, nothing
 // enqueued, when no tensor map can describe the pool.
-size_t attend_tiles_workspace(int32_t num_seqs, int64_t n_tokens, int32_t num_layers, int32_t hq,
-                              int32_t hk, int32_t head_dim);
+size_t attend_tiles_workspace(int32_t num_seqs, int32_t num_layers, int32_t hk, int32_t head_dim);
 cudaError_t launch_attend_tiles(const AttendArgs& a, cudaStream_t stream, bool* launched);
 
 // Tensor maps of the pool's codes, [unit = (layer, page, head)][row of the page][dim],
@@ -72,35 +71,19 @@ __device__ __forceinline__ int64_t item_base(const AttendArgs& a, int64_t b) {
   return static_cast<int64_t>(__ldg(a.batch.cu + b)) * a.group / R + b;
 }
 
+// Tokens that a query at position pos - 1 of sequence b sees, within the table; *cut
+// when it would see more.
+__device__ __forceinline__ int64_t visible(const AttendArgs& a, int32_t row, int64_t pos, bool* cut) {
+  const int64_t cap = row < 0 ? 0 : static_cast<int64_t>(a.table.max_pages) << a.pool.page_shift;
+  *cut = pos > cap;
+  return max(static_cast<int64_t>(0), min(pos, cap));
+}
+
+// Row tile rt of sequence b, which has packed tokens [t0, t1) and rows in that tile.
 template <int R>
-__device__ __forceinline__ Item find_item(const AttendArgs& a, int32_t bi, bool* bad) {
+__device__ __forceinline__ Item make_item(const AttendArgs& a, int32_t b, int64_t t0, int64_t t1,
+                                          int32_t rt) {
   Item it{};
-  int32_t b, rt;
-  int64_t t0, t1;
-  if (a.batch.cu == nullptr) {
-    const int32_t per = (a.group + R - 1) / R;
-    b = bi / per;
-    rt = bi - b * per;
-    t0 = b;
-    t1 = b + 1;
-  } else {
-    int32_t lo = 0, hi = a.batch.num_seqs;
-    while (hi - lo > 1) {
-      const int32_t mid = (lo + hi) >> 1;
-      if (item_base<R>(a, mid) <= bi)
-        lo = mid;
-      else
-        hi = mid;
-    }
-    b = lo;
-    if (!seq_range(a.batch, b, t0, t1)) {
-      *bad = true;
-      return it;
-    }
-    const int64_t r = bi - item_base<R>(a, b);
-    if (r < 0 || r * R >= (t1 - t0) * a.group) return it;
-    rt = static_cast<int32_t>(r);
-  }
   const int64_t all = (t1 - t0) * a.group;
   it.b = b;
   it.first_row = rt * R;
@@ -108,13 +91,34 @@ __device__ __forceinline__ Item find_item(const AttendArgs& a, int32_t bi, bool*
   it.tok = t0;
   it.p0 = a.batch.pos_offset ? __ldg(a.batch.pos_offset + b) : 0;
   it.row = table_row(a.table, b);
-  const int64_t cap = it.row < 0 ? 0 : static_cast<int64_t>(a.table.max_pages) << a.pool.page_shift;
-  const int64_t f = it.p0 + it.first_row / a.group + 1;
-  const int64_t l = it.p0 + (it.first_row + it.rows - 1) / a.group + 1;
-  it.cut = l > cap;
-  it.vis_first = max(static_cast<int64_t>(0), min(f, cap));
-  it.vis_last = max(static_cast<int64_t>(0), min(l, cap));
+  it.vis_first = visible(a, it.row, it.p0 + it.first_row / a.group + 1, &it.cut);
+  it.vis_last = visible(a, it.row, it.p0 + (it.first_row + it.rows - 1) / a.group + 1, &it.cut);
   return it;
+}
+
+template <int R>
+__device__ __forceinline__ Item find_item(const AttendArgs& a, int32_t bi, bool* bad) {
+  if (a.batch.cu == nullptr) {
+    const int32_t per = (a.group + R - 1) / R;
+    const int32_t b = bi / per;
+    return make_item<R>(a, b, b, b + 1, bi - b * per);
+  }
+  int32_t lo = 0, hi = a.batch.num_seqs;
+  while (hi - lo > 1) {
+    const int32_t mid = (lo + hi) >> 1;
+    if (item_base<R>(a, mid) <= bi)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  int64_t t0, t1;
+  if (!seq_range(a.batch, lo, t0, t1)) {
+    *bad = true;
+    return Item{};
+  }
+  const int64_t rt = bi - item_base<R>(a, lo);
+  if (rt < 0 || rt * R >= (t1 - t0) * a.group) return Item{};
+  return make_item<R>(a, lo, t0, t1, static_cast<int32_t>(rt));
 }
 
 #endif  // __CUDACC__

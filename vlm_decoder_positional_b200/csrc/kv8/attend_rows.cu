@@ -1082,7 +1082,7 @@ cudaError_t launch_attend(const AttendArgs& a, cudaStream_t stream) {
 size_t attend_workspace_bytes(int32_t num_seqs, int64_t n_tokens, int32_t num_layers, int32_t hq,
                               int32_t hk, int32_t head_dim) {
   const size_t rows = attend_rows_workspace(num_seqs, n_tokens, hq, hk, head_dim);
-  const size_t tiles = attend_tiles_workspace(num_seqs, n_tokens, num_layers, hq, hk, head_dim);
+  const size_t tiles = attend_tiles_workspace(num_seqs, num_layers, hk, head_dim);
   return rows > tiles ? rows : tiles;
 }
 

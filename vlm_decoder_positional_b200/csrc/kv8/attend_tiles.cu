@@ -50,7 +50,7 @@ constexpr int kSoftmax = 256;  // threads
 constexpr int kCleaners = 64;
 constexpr int kFirstWarp = 4;  // of the softmax
 constexpr int kThreads = kSoftmax + 32 * kFirstWarp;
-constexpr int kMaxSplits = 16;
+constexpr int kPlanned = 256;   // sequences of a call whose items are split
 constexpr float kBase = 9.f;   // weights are at most 2^9 when the reference moves
 constexpr float kLazy = 6.f;   // and 2^15 before it does
 constexpr uint32_t kColumns = 512;
@@ -82,10 +82,113 @@ struct Smem {
 
 struct TilesArgs {
   AttendArgs a;
-  int32_t items;   // slots per (layer, head)
-  int32_t splits;  // CTAs of an item
-  float* partial;  // [layers x heads x items][splits][128][D], then the rows' ref and sum
+  int32_t items;    // slots per (layer, head)
+  int32_t sms;      // multiprocessors among which items are split; 0: no item is split
+  int32_t* count;   // split items of a head in this call
+  int32_t room;     // for split items, of a head
+  int4* split;      // [heads][room]: what the joining kernel has to know of each
+  float* partial;   // [sms] records of a piece: [128][D], then the rows' ref and sum
 };
+
+// An item's share of the device: it is walked by n CTAs of `tiles` tiles each, the
+// last one of fewer.
+struct Piece {
+  Item it;
+  int32_t lh;    // layer x heads + head, or -1: none
+  int32_t all;   // tiles that the item's last row sees
+  int32_t tiles;
+  int32_t z, n;  // this one's number, of n
+  int32_t rec;   // record of the item's first piece, in the head's part
+  int32_t split; // number of the item among the head's split ones; of no piece: how many they are
+};
+
+// Items of sequence b, or 0, and the tiles that its last row sees.
+__device__ __forceinline__ void weigh(const AttendArgs& a, int32_t b, uint32_t& m, uint32_t& tiles,
+                                      bool& odd) {
+  m = tiles = 0;
+  if (b >= a.batch.num_seqs) return;
+  int64_t lo, hi;
+  bool cut;
+  odd |= !seq_range(a.batch, b, lo, hi);
+  const int64_t p0 = a.batch.pos_offset ? __ldg(a.batch.pos_offset + b) : 0;
+  const int64_t vis = visible(a, table_row(a.table, b), p0 + hi - lo, &cut);
+  m = static_cast<uint32_t>(((hi - lo) * a.group + kRows - 1) / kRows);
+  tiles = static_cast<uint32_t>(max(static_cast<int64_t>(1), (vis + kTile - 1) / kTile));
+}
+
+// Piece x of the call; asked by whole warps.  With T tiles in all items (those of a
+// sequence's last row tile counted for each of its items) and S multiprocessors, an item
+// of t tiles is cut in t S / T pieces, rounded down: the items that are cut have S pieces
+// at most, S / heads in each head, and no piece is twice as long as what each
+// multiprocessor has to do on average.  Short code: it is fetched anew by every call.
+__device__ __forceinline__ Piece find_piece(const TilesArgs& ta, uint32_t x, bool* bad) {
+  const AttendArgs& a = ta.a;
+  const int lane = threadIdx.x & 31;
+  const uint32_t heads = static_cast<uint32_t>(a.pool.num_layers) * a.pool.hk;
+  const uint32_t at = x / heads;
+  Piece p{};
+  p.lh = -1;
+  uint32_t m, n;
+  bool odd = false;
+  unsigned long long tiles = 0;
+#pragma unroll 1
+  for (int32_t b = lane; b - lane < a.batch.num_seqs; b += 32) {
+    weigh(a, b, m, n, odd);
+    tiles += static_cast<unsigned long long>(m) * n;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) tiles += __shfl_xor_sync(~0u, tiles, o);
+  // sequences out of order may overlap: nothing is split then
+  odd = __any_sync(~0u, odd);
+  *bad |= odd;
+  // a little less than S / T, so that rounding adds no piece
+  const float per_tile = odd ? 0.f : ta.sms * (1.f - 0x1p-16f) /
+                                         (static_cast<float>(tiles) * static_cast<float>(heads));
+  uint32_t base = 0, rec = 0;  // pieces, and records + 2^16 x split items, of the sequences before
+#pragma unroll 1
+  for (int32_t b = lane; b - lane < a.batch.num_seqs; b += 32) {
+    if (a.batch.num_seqs > 32) weigh(a, b, m, n, odd);
+    n = max(1u, min(n, static_cast<uint32_t>(n * per_tile)));
+    const uint32_t mine = m * n, recs = n > 1 ? mine + (m << 16) : 0u;
+    uint32_t end = mine, rec_end = recs;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t u = __shfl_up_sync(~0u, end, o), v = __shfl_up_sync(~0u, rec_end, o);
+      if (lane >= o) {
+        end += u;
+        rec_end += v;
+      }
+    }
+    end += base;
+    rec_end += rec;
+    const uint32_t here = __ballot_sync(~0u, at >= end - mine && at < end);
+    if (here) {
+      const int from = __ffs(here) - 1;
+      const uint32_t pieces = __shfl_sync(~0u, n, from);
+      const uint32_t k = at - __shfl_sync(~0u, end - mine, from);
+      const uint32_t first = __shfl_sync(~0u, rec_end - recs, from);
+      const uint32_t last = __shfl_sync(~0u, m, from) - 1;
+      b += from - lane;
+      int64_t lo, hi;
+      seq_range(a.batch, b, lo, hi);
+      // the last row tiles, which see most, come first
+      const uint32_t item = k / pieces;
+      p.it = make_item<kRows>(a, b, lo, hi, static_cast<int32_t>(last - item));
+      p.lh = static_cast<int32_t>(x - at * heads);
+      p.n = static_cast<int32_t>(pieces);
+      p.z = static_cast<int32_t>(k - item * pieces);
+      p.all = max(1, (static_cast<int>(p.it.vis_last) + kTile - 1) / kTile);
+      p.tiles = (p.all + p.n - 1) / p.n;
+      p.rec = static_cast<int32_t>((first & 0xffffu) + item * pieces);
+      p.split = static_cast<int32_t>((first >> 16) + item);
+      return p;
+    }
+    base = __shfl_sync(~0u, end, 31);
+    rec = __shfl_sync(~0u, rec_end, 31);
+  }
+  p.split = static_cast<int32_t>(rec >> 16);
+  return p;
+}
 
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t r;
@@ -102,9 +205,6 @@ __device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
 __device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
   return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
 }
-
-// The split of an item's tiles: tiles of one CTA, and how many CTAs have any.
-__device__ __forceinline__ int split_tiles(int nt, int splits) { return (nt + splits - 1) / splits; }
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -142,26 +242,45 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   pdl::wait();
   // ---- the item: heavy (late) row tiles first
-  const int32_t bi = ta.items - 1 - static_cast<int32_t>(blockIdx.x);
-  const int64_t lh = blockIdx.y;
   bool bad = false;
-  const Item it = find_item<kRows>(a, bi, &bad);
-  if (tid == 0 && a.status != nullptr && lh == 0 && blockIdx.z == 0) {
+  Piece piece;
+  if (ta.sms > 0) {
+    piece = find_piece(ta, blockIdx.x, &bad);
+    const int per = ta.sms / (a.pool.num_layers * a.pool.hk);
+    if (tid == 0) {
+      // the last slot is never a piece, unless sequences overlap
+      if (blockIdx.x == gridDim.x - 1) *ta.count = piece.lh < 0 ? piece.split : 0;
+      if (piece.n > 1 && piece.z == 0) {
+        const int n = (piece.all + piece.tiles - 1) / piece.tiles;
+        ta.split[piece.lh * ta.room + piece.split] =
+            make_int4((n > 1 ? n << 8 : 0) + piece.it.rows, piece.it.first_row,
+                      static_cast<int>(piece.it.tok), piece.rec);
+      }
+    }
+    piece.rec += piece.lh * per;
+  } else {
+    const int32_t lh = static_cast<int32_t>(blockIdx.x) / ta.items;
+    piece.it = find_item<kRows>(
+        a, ta.items - 1 - (static_cast<int32_t>(blockIdx.x) - lh * ta.items), &bad);
+    piece.lh = piece.it.rows > 0 ? lh : -1;
+    piece.all = piece.tiles = max(1, (static_cast<int>(piece.it.vis_last) + kTile - 1) / kTile);
+    piece.z = 0;
+  }
+  const Item& it = piece.it;
+  if (tid == 0 && a.status != nullptr) {
     if (bad) atomicOr(a.status, CMR_DEVICE_BAD_CU_SEQLENS);
-    if (it.rows > 0 && it.cut) atomicOr(a.status, CMR_DEVICE_CACHE_RANGE);
+    if (piece.lh == 0 && piece.z == 0 && it.cut) atomicOr(a.status, CMR_DEVICE_CACHE_RANGE);
   }
   const int vis_first = static_cast<int>(it.vis_first), vis_last = static_cast<int>(it.vis_last);
-  const int all = max(1, (vis_last + kTile - 1) / kTile);
-  const int share = split_tiles(all, ta.splits);
-  const int t0 = blockIdx.z * share;
-  const int nt = min(share, all - t0);
-  if (it.rows == 0 || nt <= 0) {
+  const int t0 = piece.z * piece.tiles;
+  const int nt = min(piece.tiles, piece.all - t0);
+  if (piece.lh < 0 || nt <= 0) {
     __syncthreads();
     if (warp == 1) tc::dealloc(*s_tmem, kColumns);
     return;
   }
-  const bool whole = share == all;
-  const int l = static_cast<int>(lh / a.pool.hk), h = static_cast<int>(lh - l * a.pool.hk);
+  const bool whole = piece.tiles == piece.all;
+  const int l = piece.lh / a.pool.hk, h = piece.lh - l * a.pool.hk;
 
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -636,8 +755,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
       }
     }
-    float* rec = ta.partial +
-                 ((lh * ta.items + bi) * ta.splits + blockIdx.z) * (kRows * (D + 2));
+    float* rec = ta.partial + static_cast<int64_t>(piece.rec + piece.z) * (kRows * (D + 2));
     if (!whole && half == 0) {
       rec[kRows * D + row] = ref;
       rec[kRows * D + kRows + row] = sum;
@@ -675,56 +793,77 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 constexpr int kJoinThreads = 256;
 
-// Joins the splits of an item: grid (items x layers x heads, row groups).
-template <int D>
+// Joins the pieces of split items: grid (room for split items, shares of the rows).  kSub
+// threads share the pieces of four dims of a row.
+template <int D, int kSub>
 __global__ void __launch_bounds__(kJoinThreads) attend_tiles_join_kernel(const TilesArgs ta) {
   const AttendArgs& a = ta.a;
   pdl::wait();
   pdl::launch_dependents();
-  const int32_t bi = static_cast<int32_t>(blockIdx.x % ta.items);
-  const int64_t lh = blockIdx.x / ta.items;
-  bool bad = false;
-  const Item it = find_item<kRows>(a, bi, &bad);
+  const int per = ta.sms / (a.pool.num_layers * a.pool.hk);
+  const int lh = blockIdx.x / ta.room;
+  if (static_cast<int>(blockIdx.x) - lh * ta.room >= __ldcg(ta.count)) return;
+  const int4 item = __ldcg(ta.split + blockIdx.x);
+  const int n = item.x >> 8;  // 0: a row tile that sees one tile only
+  const int r0 = blockIdx.y * (kJoinThreads / (D / 4) / kSub);
+  if (n == 0 || r0 >= (item.x & 0xff)) return;
+  const int l = lh / a.pool.hk, h = lh - l * a.pool.hk;
   constexpr int kLanes = D / 4;
-  const int r = blockIdx.y * (kJoinThreads / kLanes) + threadIdx.x / kLanes;
+  const int sub = threadIdx.x / kLanes % kSub;
   const int ln = threadIdx.x % kLanes;
-  if (it.rows == 0 || r >= it.rows) return;
-  const int all = max(1, (static_cast<int>(it.vis_last) + kTile - 1) / kTile);
-  const int share = split_tiles(all, ta.splits);
-  if (share == all) return;
-  const int n = (all + share - 1) / share;
-  const float* rec0 = ta.partial + (lh * ta.items + bi) * ta.splits * (kRows * (D + 2));
+  const int r = r0 + threadIdx.x / (kLanes * kSub);
+  if (kSub == 1 && r >= (item.x & 0xff)) return;
+  const float* rec0 = ta.partial + static_cast<int64_t>(lh * per + item.w) * (kRows * (D + 2));
   float top = -INFINITY;
-  for (int k = 0; k < n; ++k)
+#pragma unroll 4
+  for (int k = sub; k < n; k += kSub)
     top = fmaxf(top, __ldcg(rec0 + k * (kRows * (D + 2)) + kRows * D + r));
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float sum = 0.f;
-#pragma unroll 4
-  for (int k = 0; k < n; ++k) {
-    const float* rec = rec0 + k * (kRows * (D + 2));
-    const float ref = __ldcg(rec + kRows * D + r);
+  auto add = [&](float ref, float more, const float4& x) {
     const float w = top == -INFINITY ? 0.f : exp2_approx(ref - top);
-    const float4 x = __ldcg(reinterpret_cast<const float4*>(rec + r * D) + ln);
-    sum = fmaf(w, __ldcg(rec + kRows * D + kRows + r), sum);
+    sum = fmaf(w, more, sum);
     acc.x = fmaf(w, x.x, acc.x);
     acc.y = fmaf(w, x.y, acc.y);
     acc.z = fmaf(w, x.z, acc.z);
     acc.w = fmaf(w, x.w, acc.w);
+  };
+#pragma unroll 4
+  for (int k = sub; k < n; k += kSub) {
+    const float* rec = rec0 + k * (kRows * (D + 2));
+    add(__ldcg(rec + kRows * D + r), __ldcg(rec + kRows * D + kRows + r),
+        __ldcg(reinterpret_cast<const float4*>(rec + r * D) + ln));
+  }
+  if constexpr (kSub > 1) {
+    static_assert(kSub * kLanes == kJoinThreads, "the CTA's threads share a row");
+    __shared__ float4 s_acc[kJoinThreads];
+    __shared__ float2 s_ref[kJoinThreads];
+    s_acc[threadIdx.x] = acc;
+    s_ref[threadIdx.x] = make_float2(top, sum);
+    __syncthreads();
+    if (sub > 0) return;
+#pragma unroll
+    for (int j = 1; j < kSub; ++j) top = fmaxf(top, s_ref[j * kLanes + ln].x);
+    acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    sum = 0.f;
+#pragma unroll 4
+    for (int j = 0; j < kSub; ++j) {
+      const float2 part = s_ref[j * kLanes + ln];
+      add(part.x, part.y, s_acc[j * kLanes + ln]);
+    }
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  const int l = static_cast<int>(lh / a.pool.hk), h = static_cast<int>(lh - l * a.pool.hk);
-  const int f = it.first_row + r;
-  uint16_t* dst = a.out + ((l * a.batch.n_tokens + it.tok + f / a.group) * a.hq + h * a.group +
+  const int f = item.y + r;
+  uint16_t* dst = a.out + ((l * a.batch.n_tokens + item.z + f / a.group) * a.hq + h * a.group +
                            f % a.group) * D + 4 * ln;
   *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv),
                                               pack_bf16x2(acc.z * inv, acc.w * inv));
 }
 
-// CTAs per item: as many as fill the device once, where the items alone do not
-// fill half of it.
-int splits_for(int64_t items) {
-  const int64_t n = items > 0 ? sm_count() / items : 1;
-  return static_cast<int>(n < 1 ? 1 : (n < kMaxSplits ? n : kMaxSplits));
+// The multiprocessors that items are split among: above kPlanned sequences the plan would
+// cost more than it saves, and with more heads than half of them no item has two pieces.
+int split_among(int32_t num_seqs, int64_t heads) {
+  return num_seqs <= kPlanned && 2 * heads <= sm_count() ? sm_count() : 0;
 }
 
 template <int D>
@@ -734,29 +873,26 @@ cudaError_t launch(const TilesArgs& ta, const CUtensorMap& k, const CUtensorMap&
   cudaError_t e = cudaFuncSetAttribute(attend_tiles_kernel<D>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
   if (e != cudaSuccess) return e;
-  e = pdl::launch(attend_tiles_kernel<D>, dim3(ta.items, static_cast<unsigned>(lh), ta.splits),
-                  dim3(kThreads), S::kBytes, stream, true, ta, k, v);
-  if (e != cudaSuccess || ta.splits == 1) return e;
+  const unsigned slots = static_cast<unsigned>(ta.items * lh) + ta.sms;
+  e = pdl::launch(attend_tiles_kernel<D>, dim3(slots), dim3(kThreads), S::kBytes, stream, true, ta,
+                  k, v);
+  if (e != cudaSuccess || ta.sms == 0) return e;
+  // With few items there are many pieces of each: the threads of a CTA share those of one
+  // row.
   constexpr int kPer = kJoinThreads / (D / 4);
-  return pdl::launch(attend_tiles_join_kernel<D>,
-                     dim3(static_cast<unsigned>(ta.items * lh), kRows / kPer), dim3(kJoinThreads),
+  const unsigned room = static_cast<unsigned>(ta.room * lh);
+  if (ta.items * lh <= 16)
+    return pdl::launch(attend_tiles_join_kernel<D, kPer>, dim3(room, kRows), dim3(kJoinThreads), 0,
+                       stream, true, ta);
+  return pdl::launch(attend_tiles_join_kernel<D, 1>, dim3(room, kRows / kPer), dim3(kJoinThreads),
                      0, stream, true, ta);
 }
 
 }  // namespace
 
-size_t attend_tiles_workspace(int32_t num_seqs, int64_t n_tokens, int32_t num_layers, int32_t hq,
-                              int32_t hk, int32_t head_dim) {
-  size_t most = 0;
-  for (const bool step : {false, true}) {
-    if (step && num_seqs != n_tokens) continue;
-    const int64_t items = item_slots(num_seqs, n_tokens, hq / hk, kRows, step) * num_layers * hk;
-    const int splits = splits_for(items);
-    if (splits == 1) continue;
-    const size_t bytes = static_cast<size_t>(items) * splits * kRows * (head_dim + 2) * sizeof(float);
-    most = bytes > most ? bytes : most;
-  }
-  return most;
+size_t attend_tiles_workspace(int32_t num_seqs, int32_t num_layers, int32_t hk, int32_t head_dim) {
+  const size_t sms = split_among(num_seqs, static_cast<int64_t>(num_layers) * hk);
+  return sms == 0 ? 0 : 16 + sms * (sizeof(int4) + kRows * (head_dim + 2) * sizeof(float));
 }
 
 cudaError_t launch_attend_tiles(const AttendArgs& a, cudaStream_t stream, bool* launched) {
@@ -765,14 +901,28 @@ cudaError_t launch_attend_tiles(const AttendArgs& a, cudaStream_t stream, bool* 
   const int64_t lh = static_cast<int64_t>(pool.num_layers) * pool.hk;
   const int64_t items = item_slots(a.batch.num_seqs, a.batch.n_tokens, a.group, kRows,
                                    a.batch.cu == nullptr);
-  if (lh > 65535 || items * lh > INT32_MAX) return cudaSuccess;
+  if (items * lh > INT32_MAX - sm_count()) return cudaSuccess;
   CUtensorMap k, v;
   if (!encode_pool_maps(pool, 1u << pool.page_shift, &k, &v)) return cudaSuccess;
   TilesArgs ta{};
   ta.a = a;
   ta.items = static_cast<int32_t>(items);
-  ta.splits = splits_for(items * lh);
-  ta.partial = static_cast<float*>(a.workspace);
+  ta.sms = split_among(a.batch.num_seqs, lh);
+  // Sequences of N tokens in all see at least their own, so that the plan's T is at least
+  // heads * group * (N / 128)^2 / sequences: where even a whole row of the table has less
+  // than two pieces then, neither the plan nor the joining kernel is needed (4 prompts
+  // of 8192: 1175 us instead of 1193).
+  const double n = static_cast<double>(a.batch.n_tokens) / kTile;
+  const double row = static_cast<double>(a.table.max_pages) * (1 << pool.page_shift) / kTile + 1;
+  if (row * ta.sms < 2 * n * n * a.group / a.batch.num_seqs * static_cast<double>(lh)) ta.sms = 0;
+  if (ta.sms > 0) {
+    // a split item has two pieces or more
+    const int64_t room = ta.sms / lh / 2;
+    ta.room = static_cast<int32_t>(items < room ? items : room);
+  }
+  ta.count = static_cast<int32_t*>(a.workspace);
+  ta.split = static_cast<int4*>(a.workspace) + 1;
+  ta.partial = reinterpret_cast<float*>(ta.split + ta.sms);
   *launched = true;
   switch (pool.head_dim) {
     case 64: return launch<64>(ta, k, v, lh, stream);
