@@ -62,6 +62,18 @@ struct TileInfo {
   uint32_t valid;
 };
 
+// An item's share of the device: it is walked by n CTAs of `tiles` tiles each, the
+// last one of fewer.
+struct Piece {
+  Item it;
+  int32_t lh;    // layer x heads + head, or -1: none
+  int32_t all;   // tiles that the item's last row sees
+  int32_t tiles;
+  int32_t z, n;  // this one's number, of n
+  int32_t rec;   // record of the item's first piece, in the head's part; in the kernel, this one's
+  int32_t split; // number of the item among the head's split ones; of no piece: how many they are
+};
+
 template <int D>
 struct Smem {
   static constexpr int W = D < 128 ? D : 128;  // bytes of a swizzled row
@@ -77,7 +89,8 @@ struct Smem {
   static constexpr int kInfo = kAt + kRows * 8;
   static constexpr int kBars = (kInfo + kInfos * static_cast<int>(sizeof(TileInfo)) + 7) / 8 * 8;
   static constexpr int kMisc = kBars + 8 * (5 * kStages + 7);
-  static constexpr int kBytes = kMisc + 16 + 1024;  // and room to align
+  static constexpr int kPiece = kMisc + 16;
+  static constexpr int kBytes = kPiece + static_cast<int>(sizeof(Piece)) + 1024;  // and room to align
 };
 
 struct TilesArgs {
@@ -88,18 +101,6 @@ struct TilesArgs {
   int32_t room;     // for split items, of a head
   int4* split;      // [heads][room]: what the joining kernel has to know of each
   float* partial;   // [sms] records of a piece: [128][D], then the rows' ref and sum
-};
-
-// An item's share of the device: it is walked by n CTAs of `tiles` tiles each, the
-// last one of fewer.
-struct Piece {
-  Item it;
-  int32_t lh;    // layer x heads + head, or -1: none
-  int32_t all;   // tiles that the item's last row sees
-  int32_t tiles;
-  int32_t z, n;  // this one's number, of n
-  int32_t rec;   // record of the item's first piece, in the head's part
-  int32_t split; // number of the item among the head's split ones; of no piece: how many they are
 };
 
 // Items of sequence b, or 0, and the tiles that its last row sees.
@@ -225,6 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + S::kMisc);
   volatile int* s_dead = reinterpret_cast<volatile int*>(s_tmem + 1);
   volatile int* s_nan_taken = s_dead + 1;
+  Piece* s_piece = reinterpret_cast<Piece*>(smem + S::kPiece);
   const uint32_t q_smem = tma::smem_addr(smem + S::kQ);
   const uint32_t k_smem = tma::smem_addr(smem + S::kK);
   const uint32_t v_smem = tma::smem_addr(smem + S::kV);
@@ -241,48 +243,41 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma::prefetch_map(&v_map);
   }
   pdl::wait();
-  // ---- the item: heavy (late) row tiles first
-  bool bad = false;
-  Piece piece;
-  if (ta.sms > 0) {
-    piece = find_piece(ta, blockIdx.x, &bad);
-    const int per = ta.sms / (a.pool.num_layers * a.pool.hk);
-    if (tid == 0) {
-      // the last slot is never a piece, unless sequences overlap
-      if (blockIdx.x == gridDim.x - 1) *ta.count = piece.lh < 0 ? piece.split : 0;
-      if (piece.n > 1 && piece.z == 0) {
-        const int n = (piece.all + piece.tiles - 1) / piece.tiles;
-        ta.split[piece.lh * ta.room + piece.split] =
-            make_int4((n > 1 ? n << 8 : 0) + piece.it.rows, piece.it.first_row,
-                      static_cast<int>(piece.it.tok), piece.rec);
+  if (warp == 0) {
+    // ---- the item: heavy (late) row tiles first
+    bool bad = false;
+    Piece piece;
+    if (ta.sms > 0) {
+      piece = find_piece(ta, blockIdx.x, &bad);
+    } else {
+      const int32_t lh = static_cast<int32_t>(blockIdx.x) / ta.items;
+      piece.it = find_item<kRows>(
+          a, ta.items - 1 - (static_cast<int32_t>(blockIdx.x) - lh * ta.items), &bad);
+      piece.lh = piece.it.rows > 0 ? lh : -1;
+      piece.all = piece.tiles = max(1, (static_cast<int>(piece.it.vis_last) + kTile - 1) / kTile);
+      piece.z = 0;
+      piece.n = 1;
+    }
+    if (lane == 0) {
+      if (ta.sms > 0) {
+        // the last slot is never a piece, unless sequences overlap
+        if (blockIdx.x == gridDim.x - 1) *ta.count = piece.lh < 0 ? piece.split : 0;
+        if (piece.n > 1 && piece.z == 0) {
+          const int n = (piece.all + piece.tiles - 1) / piece.tiles;
+          ta.split[piece.lh * ta.room + piece.split] =
+              make_int4((n > 1 ? n << 8 : 0) + piece.it.rows, piece.it.first_row,
+                        static_cast<int>(piece.it.tok), piece.rec);
+        }
+        piece.rec += piece.lh * (ta.sms / (a.pool.num_layers * a.pool.hk)) + piece.z;
+      }
+      *s_piece = piece;
+      if (a.status != nullptr) {
+        if (bad) atomicOr(a.status, CMR_DEVICE_BAD_CU_SEQLENS);
+        if (piece.lh == 0 && piece.z == 0 && piece.it.cut)
+          atomicOr(a.status, CMR_DEVICE_CACHE_RANGE);
       }
     }
-    piece.rec += piece.lh * per;
-  } else {
-    const int32_t lh = static_cast<int32_t>(blockIdx.x) / ta.items;
-    piece.it = find_item<kRows>(
-        a, ta.items - 1 - (static_cast<int32_t>(blockIdx.x) - lh * ta.items), &bad);
-    piece.lh = piece.it.rows > 0 ? lh : -1;
-    piece.all = piece.tiles = max(1, (static_cast<int>(piece.it.vis_last) + kTile - 1) / kTile);
-    piece.z = 0;
-  }
-  const Item& it = piece.it;
-  if (tid == 0 && a.status != nullptr) {
-    if (bad) atomicOr(a.status, CMR_DEVICE_BAD_CU_SEQLENS);
-    if (piece.lh == 0 && piece.z == 0 && it.cut) atomicOr(a.status, CMR_DEVICE_CACHE_RANGE);
-  }
-  const int vis_first = static_cast<int>(it.vis_first), vis_last = static_cast<int>(it.vis_last);
-  const int t0 = piece.z * piece.tiles;
-  const int nt = min(piece.tiles, piece.all - t0);
-  if (piece.lh < 0 || nt <= 0) {
-    __syncthreads();
-    if (warp == 1) tc::dealloc(*s_tmem, kColumns);
-    return;
-  }
-  const bool whole = piece.tiles == piece.all;
-  const int l = piece.lh / a.pool.hk, h = piece.lh - l * a.pool.hk;
-
-  if (tid == 0) {
+  } else if (tid == 64) {
     for (int s = 0; s < kStages; ++s) {
       tma::mbar_init(k_full + 8 * s, 1);
       tma::mbar_init(k_empty + 8 * s, 1);
@@ -305,6 +300,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
+  const Item it = s_piece->it;
+  const int vis_first = static_cast<int>(it.vis_first), vis_last = static_cast<int>(it.vis_last);
+  const int t0 = s_piece->z * s_piece->tiles;
+  const int nt = min(s_piece->tiles, s_piece->all - t0);
+  if (s_piece->lh < 0 || nt <= 0) {
+    if (warp == 1) tc::dealloc(*s_tmem, kColumns);
+    return;
+  }
+  const int l = s_piece->lh / a.pool.hk, h = s_piece->lh - l * a.pool.hk;
   const uint32_t tmem = *s_tmem;
   const uint32_t tmem_s[2] = {tmem + 256, tmem + 384};
 
@@ -716,6 +720,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (nt > 1) wait(o_done, nt - 2);
     wait(o_done, nt - 1);
     tc::fence_after();
+    const bool whole = s_piece->tiles == s_piece->all;
     const float inv = !whole ? 1.f : (sum == 0.f ? 0.f : 1.f / sum);
     // Through shared memory, where Q and the keys have been used for the last time,
     // to rows that a warp writes whole: 16-byte chunks, their place turned by the
@@ -755,7 +760,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
       }
     }
-    float* rec = ta.partial + static_cast<int64_t>(piece.rec + piece.z) * (kRows * (D + 2));
+    float* rec = ta.partial + static_cast<int64_t>(s_piece->rec) * (kRows * (D + 2));
     if (!whole && half == 0) {
       rec[kRows * D + row] = ref;
       rec[kRows * D + kRows + row] = sum;
