@@ -71,8 +71,8 @@ extern "C" {
  *                     are skipped)
  * hq may be 0 (q NULL); hk >= 1.  q, k, v, k_pages and v_pages 16-byte aligned.
  * Errors: CMR_EINVAL for any violation above, CMR_EUNSUPPORTED for another
- * head_dim or page_tokens, hk * head_dim over 2^23, or num_layers * num_pages * hk or
- * (hq + hk) * num_layers over INT32_MAX. */
+ * head_dim or page_tokens, hk * head_dim over 2^23, hk * num_layers over 65535, or
+ * num_layers * num_pages * hk or (hq + hk) * num_layers over INT32_MAX. */
 CMR_API cmr_status cmr_kv8_rotate_qk(void* q, const void* k, const void* v,
                                      const int32_t* cu_seqlens, int32_t num_seqs,
                                      const int32_t* pos_offset, const int32_t* start,

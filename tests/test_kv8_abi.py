@@ -65,7 +65,7 @@ def call_write(lib, **kw):
     (dict(kp=None), 1), (dict(vp=FAKE + 4), 1), (dict(ks=None), 1), (dict(vs=FAKE + 2), 1),
     (dict(table=None), 1), (dict(start=None), 1), (dict(amount=None), 1), (dict(slot=FAKE + 1), 1),
     (dict(cu=None, seqs=3), 1), (dict(hk=1 << 20, L=1 << 12), 3), (dict(hk=1 << 16), 3),
-    (dict(pages=1 << 30, hk=4), 3), (dict(), 1),
+    (dict(pages=1 << 30, hk=4), 3), (dict(L=32768), 3), (dict(), 1),
 ])
 def test_write_rejects_bad_arguments_on_the_host(lib, kw, want):
     # the last case is well formed but for its addresses, which no device has
@@ -95,7 +95,7 @@ def call_attend(lib, **kw):
     (dict(out=FAKE), 1), (dict(out=FAKE + 16), 1), (dict(kp=FAKE + (1 << 20) + 64), 1),
     (dict(q=FAKE + 4), 1), (dict(kp=None), 1), (dict(vs=None), 1), (dict(pages=0), 1),
     (dict(table=None), 1), (dict(rows=0), 1), (dict(cols=1 << 25), 1), (dict(cu=None, seqs=4), 1),
-    (dict(L=-1), 1), (dict(), 1),
+    (dict(L=-1), 1), (dict(L=32768), 3), (dict(), 1),
 ])
 def test_attend_rejects_bad_arguments_on_the_host(lib, kw, want):
     assert call_attend(lib, **kw) == want, lib.cmr_kv8_last_error_message()

@@ -97,8 +97,8 @@ cmr_status check_pool(const void* k_pages, const void* v_pages, const float* k_s
     return fail(CMR_EUNSUPPORTED, "head_dim must be 64, 128 or 256, got %d", head_dim);
   if (page_shift(page_tokens) < 0)
     return fail(CMR_EUNSUPPORTED, "page_tokens must be 16, 32, 64 or 128, got %d", page_tokens);
-  if (static_cast<int64_t>(hk) * num_layers > INT32_MAX)
-    return fail(CMR_EUNSUPPORTED, "hk * num_layers exceeds INT32_MAX");
+  if (static_cast<int64_t>(hk) * num_layers > 65535)  // a dimension of a grid
+    return fail(CMR_EUNSUPPORTED, "hk * num_layers exceeds 65535");
   if (static_cast<int64_t>(hk) * num_layers > INT32_MAX / num_pages)
     return fail(CMR_EUNSUPPORTED, "num_layers * num_pages * hk exceeds INT32_MAX");
   if (hk > (1 << 23) / head_dim)

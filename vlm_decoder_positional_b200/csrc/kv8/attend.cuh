@@ -13,10 +13,9 @@ size_t attend_rows_workspace(int32_t num_seqs, int64_t n_tokens, int32_t hq, int
                              int32_t head_dim);
 cudaError_t launch_attend_rows(const AttendArgs& a, cudaStream_t stream);
 
-// The tcgen05 kernel for many rows (attend_tiles.cu): *launched false, nothing
-// enqueued, when no tensor map can describe the pool.
+// The tcgen05 kernel for many rows (attend_tiles.cu).
 size_t attend_tiles_workspace(int32_t num_seqs, int32_t num_layers, int32_t hk, int32_t head_dim);
-cudaError_t launch_attend_tiles(const AttendArgs& a, cudaStream_t stream, bool* launched);
+cudaError_t launch_attend_tiles(const AttendArgs& a, cudaStream_t stream);
 
 // Tensor maps of the pool's codes, [unit = (layer, page, head)][row of the page][dim],
 // for boxes of `rows` rows of up to 128 dims, swizzled by as many bytes.

@@ -24,6 +24,10 @@
 // rows of mma.m16n8k16, whose fragments are then consecutive bytes of a key, and
 // O^T += V^T P^T, whose fragments are bytes of two tokens woven together by prmt.
 // The tensor work is a few percent of the time, so tcgen05 would gain nothing.
+// Measured, 8 query and 2 KV heads of 256, pages of 64: 64 sequences of 4096 53 us
+// (5.1 TB/s, 79% of a copy's rate), one of 262144 55 us, 128 of 1 to 8192 29 us where
+// the bytes alone take 15: what is left is the start of the two kernels and the last
+// tile's way through them, about 8 us, which one sequence of 700 takes as well.
 #include "kv8.cuh"
 #include "attend.cuh"
 #include "../pdl.cuh"
@@ -983,7 +987,6 @@ cudaError_t launch(const RowsArgs& ra, const CUtensorMap& k, const CUtensorMap& 
       static_cast<int>(1024 + S::kItems + (3 * kMaxSplitItems + 1) * sizeof(int)));
   if (e != cudaSuccess) return e;
   if (ra.ctas == 0) {
-    if (lh > 65535) return cudaErrorInvalidValue;
     return pdl::launch(attend_rows_kernel<D, NQ>, dim3(ra.items, static_cast<unsigned>(lh)),
                        dim3(kThreads), smem, stream, true, ra, k, v);
   }
@@ -1065,25 +1068,30 @@ bool encode_pool_maps(const Pool& pool, uint32_t rows, CUtensorMap* k, CUtensorM
          encode_u8_tensor_map(v, pool.v, 3, dims, strides, box, static_cast<int>(W));
 }
 
+namespace {
+
+// More than 16 rows per sequence, on average: the tcgen05 kernel, which reads the
+// cache once for 128 rows.  64 sequences behind 4000, 4 query heads a group: 96 us by
+// rows and 93 by tiles for 4 tokens each, 166 and 93 for 5.  One behind 200000: 69 and
+// 77 us for 4 tokens, 120 and 77 for 8; one behind 100: 17 and 22 us for 4.
+bool by_tiles(int32_t num_seqs, int64_t n_tokens, int group) {
+  return n_tokens * group > 16 * static_cast<int64_t>(num_seqs);
+}
+
+}  // namespace
+
 cudaError_t launch_attend(const AttendArgs& a, cudaStream_t stream) {
-  // More than 16 rows per sequence, on average: the tcgen05 kernel, which reads the
-  // cache once for 128 rows.
-  if (a.batch.n_tokens * a.group > 16 * static_cast<int64_t>(a.batch.num_seqs)) {
-    bool launched = false;
-    const cudaError_t e = launch_attend_tiles(a, stream, &launched);
-    if (launched && e == cudaSuccess) note_kernel("attend_tiles_kernel");
-    if (e != cudaSuccess || launched) return e;
-  }
-  const cudaError_t e = launch_attend_rows(a, stream);
-  if (e == cudaSuccess) note_kernel("attend_rows_kernel");
+  const bool tiles = by_tiles(a.batch.num_seqs, a.batch.n_tokens, a.group);
+  const cudaError_t e = tiles ? launch_attend_tiles(a, stream) : launch_attend_rows(a, stream);
+  if (e == cudaSuccess) note_kernel(tiles ? "attend_tiles_kernel" : "attend_rows_kernel");
   return e;
 }
 
 size_t attend_workspace_bytes(int32_t num_seqs, int64_t n_tokens, int32_t num_layers, int32_t hq,
                               int32_t hk, int32_t head_dim) {
-  const size_t rows = attend_rows_workspace(num_seqs, n_tokens, hq, hk, head_dim);
-  const size_t tiles = attend_tiles_workspace(num_seqs, num_layers, hk, head_dim);
-  return rows > tiles ? rows : tiles;
+  return by_tiles(num_seqs, n_tokens, hq / hk)
+             ? attend_tiles_workspace(num_seqs, num_layers, hk, head_dim)
+             : attend_rows_workspace(num_seqs, n_tokens, hq, hk, head_dim);
 }
 
 }  // namespace kv8

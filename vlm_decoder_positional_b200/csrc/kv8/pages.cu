@@ -12,6 +12,10 @@
 // them in flight, launched to be resident when the list is ready.
 // Sources and targets of the copies of one call are disjoint by construction
 // (targets are free pages), so their order does not matter.
+// Measured, 6 layers, 2 KV heads of 256, pages of 64: 64 sequences of 2048, a quarter of
+// them freed, the pool compacted and as many grown again: 86 us, 73% of a copy's rate for
+// the pages that move; keeping the pages in flight with bulk copies through shared memory
+// instead took as long.  Four sequences freed and forked into 8 each: 18 us on the device.
 #include "kv8.cuh"
 #include "../pdl.cuh"
 
