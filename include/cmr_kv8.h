@@ -202,7 +202,10 @@ CMR_API size_t cmr_kv8_pages_workspace_bytes(int32_t table_rows, int32_t num_pag
  * for bindings to which each argument is a cost of its own.
  *   call   0 cmr_kv8_rotate_qk (28 words), 1 cmr_kv8_attend (25), 2 cmr_kv8_extend (13),
  *          3 cmr_kv8_fork (21), 4 cmr_kv8_free (9), 5 cmr_kv8_compact (17)
+ * With CMR_KV8_KNOWN_ADDRESSES added to its number a call does not look up where its
+ * addresses lie, for bindings that know them to be memory of the current device.
  * Errors: those of the call, CMR_EINVAL for another number or count of words. */
+#define CMR_KV8_KNOWN_ADDRESSES 256
 CMR_API cmr_status cmr_kv8_call(int32_t call, const void* words, int32_t count);
 
 /* Name of the kernel that the calling thread's last cmr_kv8_attend enqueued

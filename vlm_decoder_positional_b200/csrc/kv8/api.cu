@@ -7,7 +7,6 @@
 #include <cstdint>
 #include <cstdio>
 #include <cstring>
-#include <mutex>
 
 #include "kv8.cuh"
 
@@ -15,6 +14,7 @@ namespace {
 
 thread_local char g_message[320] = "no error";
 thread_local const char* g_last_kernel = nullptr;
+thread_local bool g_known = false;  // the caller knows where its addresses lie
 
 cmr_status fail(cmr_status s, const char* fmt, ...) {
   va_list ap;
@@ -62,6 +62,7 @@ struct Named {
 
 template <size_t N>
 cmr_status all_on_device(const Named (&list)[N]) {
+  if (g_known) return CMR_OK;
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess) cudaGetLastError();  // no pointer will pass then
   for (const Named& x : list) {
@@ -254,20 +255,32 @@ void note_kernel(const char* name) { g_last_kernel = name; }
 namespace kv8 {
 
 int sm_count() {
-  static std::mutex mu;
-  static int cached[64] = {};
+  static std::atomic<int> cached[64];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) {
     cudaGetLastError();
     return 0;
   }
-  std::lock_guard<std::mutex> lock(mu);
-  int& c = cached[dev & 63];
-  if (c == 0 && cudaDeviceGetAttribute(&c, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-    cudaGetLastError();
-    c = 0;
+  int c = cached[dev & 63].load(std::memory_order_relaxed);
+  if (c == 0) {
+    if (cudaDeviceGetAttribute(&c, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+      cudaGetLastError();
+      return 0;
+    }
+    cached[dev & 63].store(c, std::memory_order_relaxed);
   }
   return c;
+}
+
+cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>* done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? uint64_t{1} << dev : 0;
+  if (done->load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done->fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 
 }  // namespace kv8
@@ -500,7 +513,11 @@ cmr_status cmr_kv8_compact(void* k_pages, void* v_pages, float* k_scales, float*
 cmr_status cmr_kv8_call(int32_t call, const void* words, int32_t count) {
   if (!words) return fail(CMR_EINVAL, "words is required");
   const Words w{static_cast<const char*>(words)};
-  switch (call) {
+  struct Known {
+    explicit Known(bool known) { g_known = known; }
+    ~Known() { g_known = false; }
+  } known((call & CMR_KV8_KNOWN_ADDRESSES) != 0);
+  switch (call & ~CMR_KV8_KNOWN_ADDRESSES) {
     case 0:
       if (count != 28) break;
       return cmr_kv8_rotate_qk(w.ptr(0), w.ptr(1), w.ptr(2), w.ints(3), w.i32(4), w.ints(5),

@@ -982,9 +982,10 @@ cudaError_t launch(const RowsArgs& ra, const CUtensorMap& k, const CUtensorMap& 
   const AttendArgs& a = ra.a;
   const int64_t lh = static_cast<int64_t>(a.pool.num_layers) * a.pool.hk;
   const size_t smem = 1024 + S::kItems + (3 * (ra.ctas > 0 ? ra.items : 1) + 1) * sizeof(int);
-  cudaError_t e = cudaFuncSetAttribute(
-      attend_rows_kernel<D, NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-      static_cast<int>(1024 + S::kItems + (3 * kMaxSplitItems + 1) * sizeof(int)));
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(
+      reinterpret_cast<const void*>(attend_rows_kernel<D, NQ>),
+      static_cast<int>(1024 + S::kItems + (3 * kMaxSplitItems + 1) * sizeof(int)), &done);
   if (e != cudaSuccess) return e;
   if (ra.ctas == 0) {
     return pdl::launch(attend_rows_kernel<D, NQ>, dim3(ra.items, static_cast<unsigned>(lh)),

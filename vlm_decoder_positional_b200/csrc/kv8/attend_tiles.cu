@@ -881,8 +881,9 @@ template <int D>
 cudaError_t launch(const TilesArgs& ta, const CUtensorMap& k, const CUtensorMap& v, int64_t lh,
                    cudaStream_t stream) {
   using S = Smem<D>;
-  cudaError_t e = cudaFuncSetAttribute(attend_tiles_kernel<D>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e =
+      allow_smem(reinterpret_cast<const void*>(attend_tiles_kernel<D>), S::kBytes, &done);
   if (e != cudaSuccess) return e;
   const unsigned slots = static_cast<unsigned>(ta.items * lh) + ta.sms;
   e = pdl::launch(attend_tiles_kernel<D>, dim3(slots), dim3(kThreads), S::kBytes, stream, true, ta,

@@ -5,6 +5,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <atomic>
+
 #include "../cmr_internal.cuh"
 #include "cmr_kv8.h"
 
@@ -99,6 +101,10 @@ cudaError_t launch_compact(const PagesArgs& a, cudaStream_t stream);
 
 // SMs of the current device (cached; 0 if it cannot be read).
 int sm_count();
+
+// Lets a kernel use `bytes` of dynamic shared memory, the most it is launched with; *done
+// has a bit for each device on which that was said (it costs a tenth of a launch).
+cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>* done);
 
 #ifdef __CUDACC__
 

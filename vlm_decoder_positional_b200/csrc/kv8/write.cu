@@ -580,9 +580,10 @@ cudaError_t launch_pages(const WriteArgs& a, const FreqTable& table, cudaStream_
   const int64_t units = N / P + 2 * static_cast<int64_t>(a.batch.num_seqs);
   const size_t smem = static_cast<size_t>(P) * F * sizeof(float2);
   if (smem > 40 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(write_pages_kernel<D, P>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(smem));
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e =
+        allow_smem(reinterpret_cast<const void*>(write_pages_kernel<D, P>),
+                   static_cast<int>(P * (D / 2) * sizeof(float2)), &done);
     if (e != cudaSuccess) return e;
   }
   const int L = a.pool.num_layers;

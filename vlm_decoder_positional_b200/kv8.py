@@ -38,7 +38,8 @@ _p, _i, _l, _d, _z = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_
 _POOL = [_p, _p, _p, _p]
 
 # cmr_kv8_call's numbers, and the packing of their words: the arguments in one array cost
-# half of what ctypes takes for each of them
+# half of what ctypes takes for each of them.  The tensors are known to be on the device.
+_KNOWN_ADDRESSES = 256
 _CALLS = {"cmr_kv8_rotate_qk": (0, struct.Struct("=13qd14q")),
           "cmr_kv8_attend": (1, struct.Struct("=10qd14q")),
           "cmr_kv8_extend": (2, struct.Struct("=13q")), "cmr_kv8_fork": (3, struct.Struct("=21q")),
@@ -90,13 +91,16 @@ def lib() -> ctypes.CDLL:
     return _lib
 
 
-def _raw_stream(dev: torch.device, stream: Optional[torch.cuda.Stream]) -> int:
+# The checks below take a decode step's dozen tensors, which cost as much host time as its
+# launch: the good case is told by few comparisons, and `ix` is the device's index.
+
+def _raw_stream(ix: int, stream: Optional[torch.cuda.Stream]) -> int:
     if stream is not None:
         return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(dev.index)
+    return torch._C._cuda_getCurrentRawStream(ix)
 
 
-def _want(t, name: str, dtype: torch.dtype, dev: Optional[torch.device], shape=None) -> int:
+def _want(t, name: str, dtype: torch.dtype, ix: Optional[int], shape=None) -> int:
     """t's data pointer, after the checks (shape: a tuple, None for any size in a place)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -104,8 +108,8 @@ def _want(t, name: str, dtype: torch.dtype, dev: Optional[torch.device], shape=N
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if dev is not None and t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if ix is not None and t.get_device() != ix:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{ix}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     if shape is not None and (t.dim() != len(shape) or any(
@@ -114,37 +118,46 @@ def _want(t, name: str, dtype: torch.dtype, dev: Optional[torch.device], shape=N
     return t.data_ptr()
 
 
-def _ptr(t, name: str, dtype: torch.dtype, dev: torch.device, shape: Tuple[int, ...]) -> int:
-    """_want for a known shape: the checks of a decode step's dozen tensors cost as
-    much host time as its launch, so the good case is told by four comparisons."""
-    if isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == shape and \
-            t.get_device() == dev.index and t.is_contiguous():
-        return t.data_ptr()
-    return _want(t, name, dtype, dev, shape)
+def _ptr(t, name: str, dtype: torch.dtype, ix: int, shape: Tuple[int, ...]) -> int:
+    """_want for a known shape."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == ix and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    return _want(t, name, dtype, ix, shape)
 
 
-def _maybe(t, name, dtype, dev, shape):
-    return 0 if t is None else _ptr(t, name, dtype, dev, shape)
+def _ints(t, name: str, ix: int, n: int) -> int:
+    """_want for n int32 values."""
+    try:
+        if t.dtype is torch.int32 and t.dim() == 1 and t.numel() == n and \
+                t.get_device() == ix and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    return _want(t, name, torch.int32, ix, (n,))
 
 
-def _status(t, dev):
-    return 0 if t is None else _want(t, "device_status", torch.int32, dev)
+def _status(t, ix):
+    return 0 if t is None else _want(t, "device_status", torch.int32, ix)
 
 
-def _pool(k_pages, v_pages, k_scales, v_scales, dev):
+def _pool(k_pages, v_pages, k_scales, v_scales, ix):
     """Pointers of the pool, and (L, pages, hk, P, D)."""
-    kp = _want(k_pages, "k_pages", torch.float8_e4m3fn, dev)
+    kp = _want(k_pages, "k_pages", torch.float8_e4m3fn, ix)
     shape = k_pages.shape
     if len(shape) != 5:
         raise ValueError(f"k_pages must be [L, pages, hk, P, D], got {list(shape)}")
-    return (kp, _ptr(v_pages, "v_pages", torch.float8_e4m3fn, dev, shape),
-            _ptr(k_scales, "k_scales", torch.float32, dev, shape[:3]),
-            _ptr(v_scales, "v_scales", torch.float32, dev, shape[:3])), shape
+    heads = shape[:3]
+    return (kp, _ptr(v_pages, "v_pages", torch.float8_e4m3fn, ix, shape),
+            _ptr(k_scales, "k_scales", torch.float32, ix, heads),
+            _ptr(v_scales, "v_scales", torch.float32, ix, heads)), shape
 
 
-def _heads(t, name, dev, n=None, L=None, D=None):
+def _heads(t, name, ix, n=None, L=None, D=None):
     """(pointer, (L, N, H, D)) of bf16 [L, N, H, D] or [N, H, D]."""
-    p = _want(t, name, torch.bfloat16, dev)
+    p = _want(t, name, torch.bfloat16, ix)
     s = t.shape
     if len(s) == 3:
         s = (1, *s)
@@ -155,38 +168,40 @@ def _heads(t, name, dev, n=None, L=None, D=None):
     return p, s
 
 
-def _table(page_table, dev):
+def _table(page_table, ix):
     """(pointer, rows, columns) of page_table."""
-    p = _want(page_table, "page_table", torch.int32, dev)
+    p = _want(page_table, "page_table", torch.int32, ix)
     if page_table.dim() != 2:
         raise ValueError("page_table must be [rows, max_pages]")
     rows, cols = page_table.shape
     return p, rows, cols
 
 
-def _batch(cu_seqlens, pos_offset, slot, n, dev):
+def _batch(cu_seqlens, pos_offset, slot, n, ix):
     """(num_seqs, pointers of cu_seqlens, pos_offset and slot)."""
     if cu_seqlens is None:
         b, cu = n, 0
     else:
-        cu = _want(cu_seqlens, "cu_seqlens", torch.int32, dev)
+        cu = _want(cu_seqlens, "cu_seqlens", torch.int32, ix)
         b = cu_seqlens.numel() - 1
         if b < 0 or cu_seqlens.dim() != 1:
             raise ValueError("cu_seqlens needs num_seqs + 1 entries")
-    return b, cu, _maybe(pos_offset, "pos_offset", torch.int32, dev, (b,)), \
-        _maybe(slot, "slot", torch.int32, dev, (b,))
+    return b, cu, 0 if pos_offset is None else _ints(pos_offset, "pos_offset", ix, b), \
+        0 if slot is None else _ints(slot, "slot", ix, b)
 
 
 def _workspace(workspace, need, dev, stream):
     """(tensor, pointer, bytes): the caller's, or a new one that belongs to the stream
     that runs the call."""
     if workspace is None:
+        if need == 0:
+            return None, 0, 0
         if stream is None:
-            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
         else:
             with torch.cuda.stream(stream):
-                workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
-        return workspace, workspace.data_ptr(), max(need, 16)
+                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        return workspace, workspace.data_ptr(), need
     if not workspace.is_cuda or workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous CUDA tensor on {dev}")
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
@@ -199,18 +214,19 @@ def _sections(t, h, w):
     return a, ctypes.addressof(a)
 
 
-def _call(name: str, dev: torch.device, *args):
-    """The C function on dev, as the current device; None stands for a null pointer."""
+def _call(name: str, ix: int, *args):
+    """The C function on device ix, as the current one."""
     number, words = _CALLS[name]
     try:
         packed = words.pack(*args)
     except struct.error as e:
         raise TypeError(f"{name}: an argument is not a number of its kind ({e})") from None
     f = (_lib or lib()).cmr_kv8_call
-    if torch.cuda.current_device() == dev.index:
+    number += _KNOWN_ADDRESSES
+    if torch._C._cuda_getDevice() == ix:
         status = f(number, packed, len(packed) // 8)
     else:
-        with torch.cuda.device(dev):
+        with torch.cuda.device(ix):
             status = f(number, packed, len(packed) // 8)
     if status != CMR_OK:
         raise Kv8Error(status, name)
@@ -229,26 +245,25 @@ def rotate_qk_kv8(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor,
     into the paged 8-bit cache.  cu_seqlens=None means one token per sequence (a
     decode step); slot gives each sequence's row of page_table (default: its
     own number).  Returns q."""
-    kp, shape = _heads(k, "k", None)
-    L, n, hk, D = shape
-    dev = k.device
-    vp = _ptr(v, "v", torch.bfloat16, dev, k.shape)
+    kp, (L, n, hk, D) = _heads(k, "k", None)
+    ix = k.get_device()
+    vp = _ptr(v, "v", torch.bfloat16, ix, k.shape)
     qp, hq = 0, 0
     if q is not None:
-        qp, qs = _heads(q, "q", dev, n, L, D)
+        qp, qs = _heads(q, "q", ix, n, L, D)
         hq = qs[2]
-    pool, (pl, pages, phk, P, pd) = _pool(k_pages, v_pages, k_scales, v_scales, dev)
+    pool, (pl, pages, phk, P, pd) = _pool(k_pages, v_pages, k_scales, v_scales, ix)
     if (pl, phk, pd) != (L, hk, D):
         raise ValueError(f"k_pages must be [L, pages, hk, P, D] = [{L}, pages, {hk}, P, {D}]")
-    table, rows, cols = _table(page_table, dev)
-    b, cu, off, sl = _batch(cu_seqlens, pos_offset, slot, n, dev)
-    sp = _ptr(start, "start", torch.int32, dev, (b,))
-    ap = _ptr(amount, "amount", torch.int32, dev, (b,))
-    st = _status(device_status, dev)
+    table, rows, cols = _table(page_table, ix)
+    b, cu, off, sl = _batch(cu_seqlens, pos_offset, slot, n, ix)
+    sp = _ints(start, "start", ix, b)
+    ap = _ints(amount, "amount", ix, b)
+    st = _status(device_status, ix)
     if n and L:
-        _call("cmr_kv8_rotate_qk", dev, qp if hq else 0, kp, vp, cu, b, off, sp, ap, n, L, hq, hk, D,
+        _call("cmr_kv8_rotate_qk", ix, qp if hq else 0, kp, vp, cu, b, off, sp, ap, n, L, hq, hk, D,
               theta, _sections(*sections)[1], rot_dim, *pool, pages, P, table, rows, cols, sl, st,
-              _raw_stream(dev, stream))
+              _raw_stream(ix, stream))
     return q
 
 
@@ -281,26 +296,28 @@ def attend_kv8(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
     scale defaults to 1 / sqrt(D).  workspace: a CUDA tensor of
     attend_kv8_workspace_bytes (allocated when None).  Returns out, like q."""
     qp, (L, n, hq, D) = _heads(q, "q", None)
-    dev = q.device
-    pool, (pl, pages, hk, P, pd) = _pool(k_pages, v_pages, k_scales, v_scales, dev)
+    ix = q.get_device()
+    pool, (pl, pages, hk, P, pd) = _pool(k_pages, v_pages, k_scales, v_scales, ix)
     if (pl, pd) != (L, D):
         raise ValueError(f"k_pages must be [L, pages, hk, P, D] = [{L}, pages, hk, P, {D}]")
-    table, rows, cols = _table(page_table, dev)
-    b, cu, off, sl = _batch(cu_seqlens, pos_offset, slot, n, dev)
-    if out is None:
+    table, rows, cols = _table(page_table, ix)
+    b, cu, off, sl = _batch(cu_seqlens, pos_offset, slot, n, ix)
+    if out is not None:
+        op = _ptr(out, "out", torch.bfloat16, ix, q.shape)
+    else:
         if stream is None:
             out = torch.empty_like(q)
         else:
             with torch.cuda.stream(stream):
                 out = torch.empty_like(q)
-    op = _ptr(out, "out", torch.bfloat16, dev, q.shape)
-    st = _status(device_status, dev)
+        op = out.data_ptr()
+    st = _status(device_status, ix)
     if n and L:
-        ws, wp, wb = _workspace(workspace, _attend_bytes(dev.index, b, n, L, hq, hk, D)
-                                if workspace is None else 0, dev, stream)
-        _call("cmr_kv8_attend", dev, qp, op, cu, b, off, n, L, hq, hk, D,
+        ws, wp, wb = _workspace(workspace, _attend_bytes(ix, b, n, L, hq, hk, D)
+                                if workspace is None else 0, q.device, stream)
+        _call("cmr_kv8_attend", ix, qp, op, cu, b, off, n, L, hq, hk, D,
               D ** -0.5 if scale is None else scale, *pool, pages, P, table, rows, cols, sl, wp,
-              wb, st, _raw_stream(dev, stream))
+              wb, st, _raw_stream(ix, stream))
     return out
 
 
@@ -315,19 +332,25 @@ def kv8_pages_workspace_bytes(table_rows: int, num_pages: int, n: int = 0) -> in
     return lib().cmr_kv8_pages_workspace_bytes(table_rows, num_pages, n)
 
 
-def _pages_state(page_table, page_refs, pages=None):
-    """(device, pointer of the table, rows, columns, pointer of the counts, pages)."""
+def _pages_state(page_table, page_refs, *pool):
+    """(device index, pointers and shape of the pool, pointer of the table, rows, columns,
+    pointer of the counts, pages)."""
     t, rows, cols = _table(page_table, None)
-    dev = page_table.device
-    r = _want(page_refs, "page_refs", torch.int32, dev, (pages,))
-    return dev, t, rows, cols, r, page_refs.shape[0]
+    ix = page_table.get_device()
+    if not pool:
+        r = _want(page_refs, "page_refs", torch.int32, ix, (None,))
+        return ix, (), None, t, rows, cols, r, page_refs.numel()
+    ptrs, shape = _pool(*pool, ix)
+    r = _ints(page_refs, "page_refs", ix, shape[1])
+    return ix, ptrs, shape, t, rows, cols, r, shape[1]
 
 
-def _pages_call(name, dev, before, after, rows, pages, n, workspace, device_status, stream):
-    st = _status(device_status, dev)
+def _pages_call(name, table, before, after, rows, pages, n, workspace, device_status, stream):
+    ix = table.get_device()
+    st = _status(device_status, ix)
     ws, wp, wb = _workspace(workspace, kv8_pages_workspace_bytes(rows, pages, n)
-                            if workspace is None else 0, dev, stream)
-    _call(name, dev, *before, *after, wp, wb, st, _raw_stream(dev, stream))
+                            if workspace is None else 0, table.device, stream)
+    _call(name, ix, *before, *after, wp, wb, st, _raw_stream(ix, stream))
 
 
 def kv8_extend(page_table: torch.Tensor, page_refs: torch.Tensor, slots: torch.Tensor,
@@ -336,12 +359,12 @@ def kv8_extend(page_table: torch.Tensor, page_refs: torch.Tensor, slots: torch.T
                stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """cmr_kv8_extend: give rows slots the pages that they lack to hold lens tokens.
     Returns page_table."""
-    dev, t, rows, cols, r, pages = _pages_state(page_table, page_refs)
+    ix, _, _, t, rows, cols, r, pages = _pages_state(page_table, page_refs)
     n = slots.numel()
-    s = _ptr(slots, "slots", torch.int32, dev, (n,))
-    ln = _ptr(lens, "lens", torch.int32, dev, (n,))
+    s = _ints(slots, "slots", ix, n)
+    ln = _ints(lens, "lens", ix, n)
     if n:
-        _pages_call("cmr_kv8_extend", dev, (t, rows, cols, r, pages, page_tokens), (s, ln, n),
+        _pages_call("cmr_kv8_extend", page_table, (t, rows, cols, r, pages, page_tokens), (s, ln, n),
                     rows, pages, n, workspace, device_status, stream)
     return page_table
 
@@ -354,15 +377,14 @@ def kv8_fork(k_pages: torch.Tensor, v_pages: torch.Tensor, k_scales: torch.Tenso
              stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """cmr_kv8_fork: make the empty rows dst hold the first lens tokens of rows src,
     whole pages shared and the rest copied.  Returns page_table."""
-    dev = page_table.device
-    pool, (L, pages, hk, P, D) = _pool(k_pages, v_pages, k_scales, v_scales, dev)
-    dev, t, rows, cols, r, pages = _pages_state(page_table, page_refs, pages)
+    ix, pool, (L, _, hk, P, D), t, rows, cols, r, pages = _pages_state(
+        page_table, page_refs, k_pages, v_pages, k_scales, v_scales)
     n = src.numel()
-    s = _ptr(src, "src", torch.int32, dev, (n,))
-    d = _ptr(dst, "dst", torch.int32, dev, (n,))
-    ln = _ptr(lens, "lens", torch.int32, dev, (n,))
+    s = _ints(src, "src", ix, n)
+    d = _ints(dst, "dst", ix, n)
+    ln = _ints(lens, "lens", ix, n)
     if n:
-        _pages_call("cmr_kv8_fork", dev, pool + (L, hk, D, pages, P, t, rows, cols, r),
+        _pages_call("cmr_kv8_fork", page_table, pool + (L, hk, D, pages, P, t, rows, cols, r),
                     (s, d, ln, n), rows, pages, n, workspace, device_status, stream)
     return page_table
 
@@ -372,12 +394,12 @@ def kv8_free(page_table: torch.Tensor, page_refs: torch.Tensor, slots: torch.Ten
              stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """cmr_kv8_free: empty rows slots, one holder less for each of their pages.
     Returns page_table."""
-    dev, t, rows, cols, r, pages = _pages_state(page_table, page_refs)
+    ix, _, _, t, rows, cols, r, pages = _pages_state(page_table, page_refs)
     n = slots.numel()
-    s = _ptr(slots, "slots", torch.int32, dev, (n,))
+    s = _ints(slots, "slots", ix, n)
     if n:
-        _call("cmr_kv8_free", dev, t, rows, cols, r, pages, s, n, _status(device_status, dev),
-              _raw_stream(dev, stream))
+        _call("cmr_kv8_free", ix, t, rows, cols, r, pages, s, n, _status(device_status, ix),
+              _raw_stream(ix, stream))
     return page_table
 
 
@@ -388,10 +410,9 @@ def kv8_compact(k_pages: torch.Tensor, v_pages: torch.Tensor, k_scales: torch.Te
                 stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """cmr_kv8_compact: move pages so that those in use are the pool's first.
     Returns page_table."""
-    dev = page_table.device
-    pool, (L, pages, hk, P, D) = _pool(k_pages, v_pages, k_scales, v_scales, dev)
-    dev, t, rows, cols, r, pages = _pages_state(page_table, page_refs, pages)
+    ix, pool, (L, _, hk, P, D), t, rows, cols, r, pages = _pages_state(
+        page_table, page_refs, k_pages, v_pages, k_scales, v_scales)
     if L:
-        _pages_call("cmr_kv8_compact", dev, pool + (L, hk, D, pages, P, t, rows, cols, r), (),
+        _pages_call("cmr_kv8_compact", page_table, pool + (L, hk, D, pages, P, t, rows, cols, r), (),
                     rows, pages, 0, workspace, device_status, stream)
     return page_table
