@@ -203,6 +203,34 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return r;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// Two fp32 operations in an instruction.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float2 parts(uint64_t x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+
 __device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
   const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
   return *reinterpret_cast<const uint32_t*>(&r);
@@ -649,9 +677,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       float mx = -INFINITY;
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
-        float top = __uint_as_float(x[g / 2][g % 2 * 16]);
+        const uint32_t* y = x[g / 2] + g % 2 * 16;
+        float top = fmaxf(__uint_as_float(y[0]), __uint_as_float(y[1]));
 #pragma unroll
-        for (int j = 1; j < 16; ++j) top = fmaxf(top, __uint_as_float(x[g / 2][g % 2 * 16 + j]));
+        for (int j = 2; j < 16; j += 2)
+          top = max3(top, __uint_as_float(y[j]), __uint_as_float(y[j + 1]));
         mx = fmaxf(mx, fmaf(top, f[g], c[g]));
       }
       // the row's maximum over both halves; the two warps of these rows have read
@@ -687,15 +717,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t t1[16], t2[16], t3[16];
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
-        const float less = c[g] - shift;
-        float part[2] = {0.f, 0.f};
+        const uint64_t ff = pair(f[g], f[g]), less = pair(c[g] - shift, c[g] - shift);
+        uint64_t part = 0;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {  // 4 tokens: a word of each term
           float p[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            p[k] = exp2_approx(fmaf(__uint_as_float(x[g / 2][g % 2 * 16 + 4 * j + k]), f[g], less));
-            part[k & 1] += p[k];
+          for (int k = 0; k < 4; k += 2) {
+            const uint32_t* y = x[g / 2] + g % 2 * 16 + 4 * j + k;
+            const float2 e = parts(fma2(pair(__uint_as_float(y[0]), __uint_as_float(y[1])), ff, less));
+            p[k] = exp2_approx(e.x);
+            p[k + 1] = exp2_approx(e.y);
+            part = add2(part, pair(p[k], p[k + 1]));
           }
           // rounded to 9 significant bits, then three times 3 of them
           const uint32_t a0 = (pack_f16x2(p[0], p[1]) + 0x00020002u) & 0xfffcfffcu;
@@ -706,7 +739,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           t2[4 * g + j] = __byte_perm(b0, b1, 0x7531);
           t3[4 * g + j] = __byte_perm(c0, c1, 0x7531);
         }
-        sum = fmaf(part[0] + part[1], info.v_inv[4 * half + g], sum);
+        sum = fmaf(parts(part).x + parts(part).y, info.v_inv[4 * half + g], sum);
       }
       tc::st16(tmem_s[i & 1] + lanes + 16 * half, t1);
       tc::st16(tmem_s[i & 1] + lanes + 32 + 16 * half, t2);
