@@ -10,10 +10,10 @@
 //       value into (224, 448]: q1 keeps 4 significant bits, q2 those of the rest,
 //       together bf16's 8 (values below 2^-8 of the largest lose bits under
 //       2^-19 of it);
-//   p = p1 + p2 + p3, e5m2: e5m2 is the upper byte of f16, so with p rounded to 9
-//       significant bits in f16, p1 is its upper byte, p2 that of what is left,
-//       p3 that of the rest, exactly (down to 2^-25 of the row's largest weight).
-// p thus carries the rounding that bf16 weights would (2^-9), and S and O are fp32
+//   p = p1 + p2 + p3, e5m2: e5m2 is the upper byte of f16, so p1 is the upper byte of
+//       p in f16, p2 that of what is left, and p3 that of the rest, rounded: 9
+//       significant bits at least (down to 2^-25 of the row's largest weight).
+// p thus carries half the rounding that bf16 weights would (2^-9), and S and O are fp32
 // accumulators in tensor memory.  The scales enter as in attend_rows.cu: keys' in
 // the exponent's factor, values' in the exponent, and 2^-e in the sum of weights.
 //
@@ -730,14 +730,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             p[k + 1] = exp2_approx(e.y);
             part = add2(part, pair(p[k], p[k + 1]));
           }
-          // rounded to 9 significant bits, then three times 3 of them
-          const uint32_t a0 = (pack_f16x2(p[0], p[1]) + 0x00020002u) & 0xfffcfffcu;
-          const uint32_t a1 = (pack_f16x2(p[2], p[3]) + 0x00020002u) & 0xfffcfffcu;
+          // three times 3 significant bits, the last ones rounded
+          const uint32_t a0 = pack_f16x2(p[0], p[1]), a1 = pack_f16x2(p[2], p[3]);
           const uint32_t b0 = sub_f16x2(a0, a0 & 0xff00ff00u), b1 = sub_f16x2(a1, a1 & 0xff00ff00u);
           const uint32_t c0 = sub_f16x2(b0, b0 & 0xff00ff00u), c1 = sub_f16x2(b1, b1 & 0xff00ff00u);
           t1[4 * g + j] = __byte_perm(a0, a1, 0x7531);
           t2[4 * g + j] = __byte_perm(b0, b1, 0x7531);
-          t3[4 * g + j] = __byte_perm(c0, c1, 0x7531);
+          t3[4 * g + j] = __byte_perm(c0 + 0x00800080u, c1 + 0x00800080u, 0x7531);
         }
         sum = fmaf(parts(part).x + parts(part).y, info.v_inv[4 * half + g], sum);
       }
