@@ -26,7 +26,7 @@
 // page gets one row and the rest of the work is latency.
 // Measured, 6 layers, 8 query and 2 KV heads of 256, pages of 64: 8 prompts of 4096
 // 181 us, 86% of a copy's rate; 12 ragged chunks 17 us; a step of 256 sequences 7 us
-// and of one 4 us on the device (14 with the host's part of the call).
+// and of one 4 us on the device (12 with the host's part of the call).
 #include "kv8.cuh"
 #include "../pdl.cuh"
 #include "../rotate_common.cuh"
