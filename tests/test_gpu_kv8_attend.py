@@ -402,3 +402,57 @@ def test_refusals(cuda_device):
                     (dict(page_table=c.table.long()), TypeError)]:
         with pytest.raises(err):
             ok(**kw)
+
+
+def test_queries_beyond_four_gigabytes(cuda_device):
+    # elements of Q, K, V and the result whose indices pass 31 bits: the last sequences of a
+    # large call are what they are alone
+    dev = cuda_device
+    n, T, D, P, hk = 1 << 20, 512, 256, 128, 9
+    B, pages = n // T, T // P
+    g = torch.Generator(device=dev).manual_seed(3)
+    text = lambda m: (i32([1 << 30] * m, dev), i32([0] * m, dev))
+    cu = i32(np.arange(B + 1) * T, dev)
+    k = torch.empty((1, n, hk, D), dtype=torch.bfloat16, device=dev).normal_(generator=g)
+    v = k.flip(1)
+    table = torch.arange(B * pages, dtype=torch.int32, device=dev).view(B, pages)
+    codes = lambda m: torch.zeros((1, m, hk, P, D), dtype=torch.uint8, device=dev).view(
+        torch.float8_e4m3fn)
+    pool = (codes(B * pages), codes(B * pages), *(torch.ones((1, B * pages, hk), device=dev)
+                                                  for _ in range(2)))
+    pkg.rotate_qk_kv8(None, k, v, *text(B), *pool, table, cu_seqlens=cu)
+    few = (codes(pages), codes(pages), *(torch.ones((1, pages, hk), device=dev) for _ in range(2)))
+    pkg.rotate_qk_kv8(None, k[:, -T:].contiguous(), v[:, -T:].contiguous(), *text(1), *few,
+                      table[:1].contiguous(), cu_seqlens=i32([0, T], dev))
+    for whole, alone in zip(pool, few):
+        assert torch.equal(whole[:, -pages:].view(torch.uint8), alone.view(torch.uint8))
+    q = k                                        # [1, n, 9, 256]: as many query heads
+    out = pkg.attend_kv8(q, *pool, table, cu_seqlens=cu)
+    assert pkg.last_attend_kernel() == "attend_tiles_kernel"
+    want = pkg.attend_kv8(q[:, -T:].contiguous(), *pool, table[-1:].contiguous(),
+                          cu_seqlens=i32([0, T], dev))
+    # each is within half a step of bf16 and 2^-9 of the mean magnitude of the exact result
+    mean = float(want.float().abs().max())
+    assert float((out[:, -T:].float() - want.float()).abs().max()) <= (2 * 2 ** -8 + 2 * 2 ** -9) * \
+        max(mean, float(v.float().abs().max()))
+    # a step of as many sequences, all of which read one row
+    slot = torch.full((n,), B - 1, dtype=torch.int32, device=dev)
+    off = torch.full((n,), T - 1, dtype=torch.int32, device=dev)
+    pkg.attend_kv8(q, *pool, table, pos_offset=off, slot=slot, out=out)
+    assert pkg.last_attend_kernel() == "attend_rows_kernel"
+    one = pkg.attend_kv8(q[:, -3000:].contiguous(), *pool, table, pos_offset=off[:3000].contiguous(),
+                         slot=slot[:3000].contiguous())
+    assert torch.equal(out[:, -3000:], one)
+
+
+def test_sequences_without_tokens_leave_everything_as_it_was(cuda_device):
+    dev = cuda_device
+    c = Cache(dev, [1, 1])
+    q = torch.ones((1, 70, 8, 256), device=dev, dtype=torch.bfloat16)
+    out = torch.full_like(q, 7.0)
+    for n in (70, 2):
+        status = torch.zeros(1, dtype=torch.int32, device=dev)
+        pkg.attend_kv8(q[:, :n].contiguous(), *c.pool(), c.table, cu_seqlens=i32([0, 0, 0], dev),
+                       out=out[:, :n].contiguous() if n < 70 else out, device_status=status)
+        assert int(status.item()) == 0
+    assert torch.equal(out, torch.full_like(out, 7.0))
