@@ -82,6 +82,12 @@ def test_more_sequences_than_are_split_evenly(cuda_device, L):
     run(cuda_device, [1] * 2100, rng.integers(0, 70, 2100), L=L, hq=2, hk=1, D=64, P=16, step=True)
 
 
+@pytest.mark.parametrize("longest", [319, 320])   # with its token: 5 tiles of 64, and one more
+def test_tables_of_a_few_pages(cuda_device, longest):
+    run(cuda_device, [1] * 5, [longest, 0, 5, 63, 64], P=16, step=True, kernel="attend_rows_kernel")
+    run(cuda_device, [2, 3, 1], [longest - 1, 60, 0], D=64, P=16, kernel="attend_rows_kernel")
+
+
 def test_one_long_sequence(cuda_device):
     run(cuda_device, [1], [70000], hq=8, hk=2, D=128, P=128, step=True)
     run(cuda_device, [40], [20000], hq=8, hk=2, D=128, P=16)

@@ -48,6 +48,10 @@ constexpr int kConsumers = kWarps * 32;
 constexpr int kThreads = kConsumers + 32;
 constexpr int kMaxSplitItems = 2048;  // items per (layer, head) that are split evenly
 constexpr int kMaxCtas = 1024;        // of the split form
+// Items of fewer tiles are not split, which saves the joining kernel: a call for 16
+// sequences of 100 or 300 tokens takes 12.8 us instead of 15.0, of 700 16.9 instead of
+// 15.5 (in tables of no more pages than they need).
+constexpr int kMinSplitTiles = 6;
 constexpr float kLazy = 8.f;    // the reference moves once weights pass 2^8
 
 struct StageInfo {
@@ -1037,7 +1041,7 @@ cudaError_t launch_attend_rows(const AttendArgs& a, cudaStream_t stream) {
   const int64_t cap = static_cast<int64_t>(a.table.max_pages) << a.pool.page_shift;
   const int64_t most_tiles = ((cap + kTile - 1) / kTile + kLead) * nb;  // per layer and head
   const int64_t lh = static_cast<int64_t>(a.pool.num_layers) * a.pool.hk;
-  if (nb <= kMaxSplitItems && most_tiles <= INT32_MAX / lh) {
+  if (nb <= kMaxSplitItems && cap > (kMinSplitTiles - 1) * kTile && most_tiles <= INT32_MAX / lh) {
     ra.prefix = static_cast<int32_t*>(a.workspace);
     ra.left = reinterpret_cast<int4*>(static_cast<uint8_t*>(a.workspace) +
                                       align16((nb + 1) * sizeof(int32_t)));
