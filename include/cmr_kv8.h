@@ -110,10 +110,12 @@ CMR_API cmr_status cmr_kv8_rotate_qk(void* q, const void* k, const void* v,
  *                     CMR_DEVICE_WAIT_TIMEOUT
  *   the rest          as in cmr_kv8_rotate_qk
  * Scores (scale * q . k) have to lie within fp32's range.
- * Calls of one token per sequence, or of a few, run a kernel that shares each key and
- * value among 8 or 16 rows and is bound by reading the cache; calls of more than 16
- * rows (tokens x hq / hk) per sequence on average run one of 128 rows on the
- * tensor cores.  A batch of both kinds is quicker as two calls.
+ * One kernel shares each key and value among 8 or 16 query rows (tokens x hq / hk) and
+ * is bound by reading the cache, another takes 128 rows on the tensor cores.  A decode
+ * step runs the first for hq / hk up to 16.  With cu_seqlens, whose lengths only the
+ * device knows, a call of more than 64 rows runs the second when there are more than
+ * 8 rows per sequence on average, and otherwise both, the second for the sequences
+ * of more than 32 rows.
  * Errors: as cmr_kv8_rotate_qk, and CMR_EINVAL when max_pages * page_tokens is over
  * INT32_MAX - 256. */
 CMR_API cmr_status cmr_kv8_attend(const void* q, void* out, const int32_t* cu_seqlens,
@@ -209,7 +211,8 @@ CMR_API size_t cmr_kv8_pages_workspace_bytes(int32_t table_rows, int32_t num_pag
 CMR_API cmr_status cmr_kv8_call(int32_t call, const void* words, int32_t count);
 
 /* Name of the kernel that the calling thread's last cmr_kv8_attend enqueued
- * ("attend_rows_kernel" or "attend_tiles_kernel"); "" before the first. */
+ * ("attend_rows_kernel", "attend_tiles_kernel", or both with ", " between); "" before
+ * the first. */
 CMR_API const char* cmr_kv8_last_attend_kernel(void);
 
 /* One-line reason for the last non-CMR_OK return of a cmr_kv8_ call on the calling

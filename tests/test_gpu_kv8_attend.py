@@ -108,10 +108,38 @@ def test_items_cut_in_pieces(cuda_device, lens, offs, shape):
     # whatever the workspace holds before
     L, D, hq, hk = (shape.get(k, d) for k, d in (("L", 1), ("D", 256), ("hq", 8), ("hk", 2)))
     need = pkg.attend_kv8_workspace_bytes(len(lens), sum(lens), L, hq, hk, D)
-    kernel = "attend_tiles_kernel" if sum(lens) * hq // hk > 16 * len(lens) else "attend_rows_kernel"
     for fill in (0x7F, 0xFF):
         ws = torch.full((need,), fill, dtype=torch.uint8, device=cuda_device)
-        run(cuda_device, lens, offs, kernel=kernel, workspace=ws, **shape)
+        run(cuda_device, lens, offs, kernel="attend_tiles_kernel", workspace=ws, **shape)
+
+
+BOTH = "attend_rows_kernel, attend_tiles_kernel"
+
+
+@pytest.mark.parametrize("D, P", [(64, 16), (128, 128), (256, 64)])
+@pytest.mark.parametrize("lens, offs", [
+    ([1] * 60 + [8, 9, 33], [50, 900, 3] * 20 + [700, 64, 4000]),     # 32, 36 and 132 rows
+    ([33] + [1] * 40, [5000] + [0, 63, 64, 300] * 10),
+    ([0, 2] * 16 + [16, 0], [100] * 34),
+    ([1] * 300 + [200], [70] * 300 + [1000])])                        # more than are planned
+def test_decode_steps_beside_a_chunk(cuda_device, lens, offs, D, P):
+    need = pkg.attend_kv8_workspace_bytes(len(lens), sum(lens) + 5, 1, 8, 2, D)
+    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device=cuda_device)
+    a, q, c = run(cuda_device, lens, offs, D=D, P=P, kernel=BOTH, workspace=ws, tail=5)
+    cu = i32(np.concatenate([[0], np.cumsum(lens)]), cuda_device)
+    b = pkg.attend_kv8(q, *c.pool(), c.table, cu_seqlens=cu, pos_offset=i32(offs, cuda_device))
+    n = sum(lens)
+    assert torch.equal(a[:, :n], b[:, :n])
+
+
+def test_malformed_decode_steps_beside_a_chunk_are_flagged(cuda_device):
+    dev = cuda_device
+    c = Cache(dev, [4] * 40)
+    q = torch.ones((1, 70, 8, 256), device=dev, dtype=torch.bfloat16)
+    for cu in ([0, 75] + [70] * 39, [0, -1] + [70] * 39, list(range(20)) + [60, 30] + [70] * 19):
+        status = torch.zeros(1, dtype=torch.int32, device=dev)
+        pkg.attend_kv8(q, *c.pool(), c.table, cu_seqlens=i32(cu, dev), device_status=status)
+        assert pkg.last_attend_kernel() == BOTH and int(status.item()) & 1
 
 
 def test_a_step_of_a_large_group_cut_in_pieces(cuda_device):

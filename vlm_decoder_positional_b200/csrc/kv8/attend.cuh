@@ -95,6 +95,10 @@ __device__ __forceinline__ Item make_item(const AttendArgs& a, int32_t b, int64_
   return it;
 }
 
+__device__ __forceinline__ bool takes(const AttendArgs& a, int64_t rows) {
+  return rows >= a.min_rows && rows <= a.max_rows;
+}
+
 template <int R>
 __device__ __forceinline__ Item find_item(const AttendArgs& a, int32_t bi, bool* bad) {
   if (a.batch.cu == nullptr) {
@@ -115,6 +119,7 @@ __device__ __forceinline__ Item find_item(const AttendArgs& a, int32_t bi, bool*
     *bad = true;
     return Item{};
   }
+  if (!takes(a, (t1 - t0) * a.group)) return Item{};
   const int64_t rt = bi - item_base<R>(a, lo);
   if (rt < 0 || rt * R >= (t1 - t0) * a.group) return Item{};
   return make_item<R>(a, lo, t0, t1, static_cast<int32_t>(rt));

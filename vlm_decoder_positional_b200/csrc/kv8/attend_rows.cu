@@ -1075,28 +1075,66 @@ bool encode_pool_maps(const Pool& pool, uint32_t rows, CUtensorMap* k, CUtensorM
 
 namespace {
 
-// More than 16 rows per sequence, on average: the tcgen05 kernel, which reads the
-// cache once for 128 rows.  64 sequences behind 4000, 4 query heads a group: 96 us by
-// rows and 93 by tiles for 4 tokens each, 166 and 93 for 5.  One behind 200000: 69 and
-// 77 us for 4 tokens, 120 and 77 for 8; one behind 100: 17 and 22 us for 4.
-bool by_tiles(int32_t num_seqs, int64_t n_tokens, int group) {
-  return n_tokens * group > 16 * static_cast<int64_t>(num_seqs);
+// Which kernels a call needs.  The tcgen05 kernel reads the cache once for 128 rows: for
+// more than 16 rows per sequence on average (64 sequences behind 4000, 4 query heads a
+// group: 96 us by rows and 93 by tiles for 4 tokens each, 166 and 93 for 5; one behind
+// 200000: 69 and 77 us for 4 tokens, 120 and 77 for 8; one behind 100: 17 and 22 us for
+// 4), and for more than 8 where the tokens, whose shares only the device knows, may be
+// one sequence's.  Up to 8, such a call is shared out: the sequences of more than
+// kFewRows rows go to the one kernel, the others to the other.  63 sequences of one
+// token behind 2000 and one of 60 behind 100000 take 120 us so and 428 by rows alone, one
+// of 128 179 and 876; that costs 8 us where there was nothing to share out (64 of one
+// token behind 4000, called with cu_seqlens: 63 us instead of 55).
+constexpr int kSmallCall = 64;  // rows in all, for which a second kernel does not pay
+constexpr int kFewRows = 32;
+
+struct Kernels {
+  bool rows, tiles;
+};
+
+Kernels kernels_of(int32_t num_seqs, int64_t n_tokens, int group, bool step) {
+  const int64_t rows = n_tokens * group;
+  const bool uneven = !step && num_seqs > 1 && rows > kSmallCall;
+  const bool tiles = rows > (uneven ? 8 : 16) * static_cast<int64_t>(num_seqs);
+  return {!tiles, tiles || uneven};
 }
 
 }  // namespace
 
-cudaError_t launch_attend(const AttendArgs& a, cudaStream_t stream) {
-  const bool tiles = by_tiles(a.batch.num_seqs, a.batch.n_tokens, a.group);
-  const cudaError_t e = tiles ? launch_attend_tiles(a, stream) : launch_attend_rows(a, stream);
-  if (e == cudaSuccess) note_kernel(tiles ? "attend_tiles_kernel" : "attend_rows_kernel");
-  return e;
+cudaError_t launch_attend(const AttendArgs& args, cudaStream_t stream) {
+  AttendArgs a = args;
+  const Kernels k = kernels_of(a.batch.num_seqs, a.batch.n_tokens, a.group, a.batch.cu == nullptr);
+  a.min_rows = 0;
+  a.max_rows = k.rows && k.tiles ? kFewRows : INT64_MAX;
+  if (k.rows) {
+    const cudaError_t e = launch_attend_rows(a, stream);
+    if (e != cudaSuccess) return e;
+    a.min_rows = kFewRows + 1;
+    a.max_rows = INT64_MAX;
+  }
+  if (k.tiles) {
+    const cudaError_t e = launch_attend_tiles(a, stream);
+    if (e != cudaSuccess) return e;
+  }
+  note_kernel(!k.tiles ? "attend_rows_kernel"
+                       : (k.rows ? "attend_rows_kernel, attend_tiles_kernel" : "attend_tiles_kernel"));
+  return cudaSuccess;
 }
 
 size_t attend_workspace_bytes(int32_t num_seqs, int64_t n_tokens, int32_t num_layers, int32_t hq,
                               int32_t hk, int32_t head_dim) {
-  return by_tiles(num_seqs, n_tokens, hq / hk)
-             ? attend_tiles_workspace(num_seqs, num_layers, hk, head_dim)
-             : attend_rows_workspace(num_seqs, n_tokens, hq, hk, head_dim);
+  // both forms of a call (with and without cu_seqlens) fit; of two kernels the second
+  // begins when the first has ended
+  size_t most = 0;
+  for (const bool step : {false, true}) {
+    if (step && num_seqs != n_tokens) continue;
+    const Kernels k = kernels_of(num_seqs, n_tokens, hq / hk, step);
+    const size_t rows = k.rows ? attend_rows_workspace(num_seqs, n_tokens, hq, hk, head_dim) : 0;
+    const size_t tiles = k.tiles ? attend_tiles_workspace(num_seqs, num_layers, hk, head_dim) : 0;
+    most = rows > most ? rows : most;
+    most = tiles > most ? tiles : most;
+  }
+  return most;
 }
 
 }  // namespace kv8

@@ -117,6 +117,7 @@ __device__ __forceinline__ void weigh(const AttendArgs& a, int32_t b, uint32_t& 
   int64_t lo, hi;
   bool cut;
   odd |= !seq_range(a.batch, b, lo, hi);
+  if (!takes(a, (hi - lo) * a.group)) return;
   const int64_t p0 = a.batch.pos_offset ? __ldg(a.batch.pos_offset + b) : 0;
   const int64_t vis = visible(a, table_row(a.table, b), p0 + hi - lo, &cut);
   m = static_cast<uint32_t>(((hi - lo) * a.group + kRows - 1) / kRows);
@@ -942,8 +943,8 @@ size_t attend_tiles_workspace(int32_t num_seqs, int32_t num_layers, int32_t hk, 
 cudaError_t launch_attend_tiles(const AttendArgs& a, cudaStream_t stream) {
   const Pool& pool = a.pool;
   const int64_t lh = static_cast<int64_t>(pool.num_layers) * pool.hk;
-  const int64_t items = item_slots(a.batch.num_seqs, a.batch.n_tokens, a.group, kRows,
-                                   a.batch.cu == nullptr);
+  int64_t items = item_slots(a.batch.num_seqs, a.batch.n_tokens, a.group, kRows,
+                             a.batch.cu == nullptr);
   if (items * lh > INT32_MAX - sm_count()) return cudaErrorInvalidValue;
   CUtensorMap k, v;
   if (!encode_pool_maps(pool, 1u << pool.page_shift, &k, &v)) return cudaErrorNotSupported;
@@ -959,6 +960,11 @@ cudaError_t launch_attend_tiles(const AttendArgs& a, cudaStream_t stream) {
   const double row = static_cast<double>(a.table.max_pages) * (1 << pool.page_shift) / kTile + 1;
   if (row * ta.sms < 2 * n * n * a.group / a.batch.num_seqs * static_cast<double>(lh)) ta.sms = 0;
   if (ta.sms > 0) {
+    if (a.min_rows > 0) {
+      // no more sequences than have so many rows, and a tile of each is not full
+      const int64_t rows = a.batch.n_tokens * a.group, most = rows / kRows + rows / a.min_rows;
+      ta.items = static_cast<int32_t>(items = items < most ? items : most);
+    }
     // a split item has two pieces or more
     const int64_t room = ta.sms / lh / 2;
     ta.room = static_cast<int32_t>(items < room ? items : room);

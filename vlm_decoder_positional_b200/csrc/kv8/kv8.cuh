@@ -71,6 +71,7 @@ struct AttendArgs {
   Table table;
   void* workspace;
   int32_t* status;
+  int64_t min_rows, max_rows;  // the sequences to take: those of so many query rows
 };
 
 cudaError_t launch_write(const WriteArgs& a, const FreqTable& table, cudaStream_t stream);
