@@ -272,12 +272,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t o_done = s_full + 32, q_ready = s_full + 40, drained = s_full + 48;
   const uint32_t v_clean = s_full + 56;
 
-  if (warp == 1) tc::alloc(tma::smem_addr(s_tmem), kColumns);
   if (tid == 0) {
     tma::prefetch_map(&k_map);
     tma::prefetch_map(&v_map);
   }
   pdl::wait();
+  // Not before the wait: the kernel ahead may be another's, which signals before it takes
+  // tensor memory of its own; it would wait for these columns and this CTA for its end.
+  if (warp == 1) tc::alloc(tma::smem_addr(s_tmem), kColumns);
   if (warp == 0) {
     // ---- the item: heavy (late) row tiles first
     bool bad = false;
