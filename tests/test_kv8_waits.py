@@ -39,3 +39,11 @@ def test_no_tensor_memory_is_held_before_the_wait(name):
     # kernel would wait for good, and so would that kernel's allocation
     before, wait, _ = KERNELS[name].partition("pdl::wait();")
     assert wait and "alloc" not in before
+
+
+@pytest.mark.parametrize("name", sorted(KERNELS))
+def test_no_memory_is_read_before_the_wait(name):
+    # no load, none by a function that reads the call's tensors, and no signal to the kernel behind
+    before = KERNELS[name].partition("pdl::wait();")[0]
+    assert not re.search(r"__ld\w*\(|\bfind_\w+|seq_range|page_id|table_row|planes_of|atomic\w+\(|"
+                         r"prefetch\.global|load_\dd|launch_dependents", before)

@@ -827,11 +827,11 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const RowsArg
   const int32_t NB = ra.items;
   const int32_t bi = static_cast<int32_t>(blockIdx.x % NB);
   const uint32_t lh = blockIdx.x / NB;
-  bool bad = false;
-  const Item it = find_item<R>(a, bi, &bad);  // of the call's inputs: no need to wait
   const int r = blockIdx.y;
   pdl::wait();
   pdl::launch_dependents();
+  bool bad = false;
+  const Item it = find_item<R>(a, bi, &bad);
   if (r >= it.rows) return;
   const uint32_t total = __ldcg(ra.prefix + NB);
   const uint32_t start = lh * total + __ldcg(ra.prefix + bi);

@@ -6,9 +6,10 @@
 // depend on it -- here, the TMA loads of Q and K, which the positions kernels
 // never touch -- overlaps the earlier kernel's tail.
 //
-// Only kernels launched behind one of this library's own kernels use the
-// attribute: a caller's kernel may signal early while it is still writing the
-// Q/K that a dependent kernel would load before its wait.
+// A kernel that reads anything before its wait is launched with the attribute only
+// behind one of this library's own kernels: a caller's kernel may signal early while
+// it is still writing the Q/K that a dependent kernel would load before its wait.
+// The kernels of kv8/ read nothing before theirs and are launched with it behind any.
 #pragma once
 
 #include <cuda_runtime.h>
