@@ -7,9 +7,12 @@
 // scale enters the weight, so codes are never multiplied by a scale, and a page
 // of large values cannot push the weights of the others out of range.  e4m3
 // codes are exact in f16; q is brought to f16 exactly by a power of two per row
-// (bits below 2^-24 of the row's largest value are lost), p is rounded to f16
-// (at most 2^-11 relative, unbiased, against the 2^-9 of the bf16 result), and all
-// sums, maxima and the accumulator are fp32.
+// (bits below 2^-24 of the row's largest value are lost).  p is rounded to f16 for the
+// product: r is placed so that the row's largest p lies between 2^13 and 2^15, so a
+// weight of 2^-27 of it or more is off by 2^-11 of itself at most (the bf16 result by
+// 2^-8), a smaller one by 2^-38 of the largest: tokens behind a strong one keep their
+// part, however many they are.  The sum of weights takes p as it is; all sums, maxima and
+// the accumulator are fp32.
 //
 // Bound by reading the cache once (1 byte per value).  The rows of a KV head's
 // query group, 8 or 16 of them, share each key and value that is read.  The work
@@ -52,7 +55,12 @@ constexpr int kMaxCtas = 1024;        // of the split form
 // sequences of 100 or 300 tokens takes 12.8 us instead of 15.0, of 700 16.9 instead of
 // 15.5 (in tables of no more pages than they need).
 constexpr int kMinSplitTiles = 6;
-constexpr float kLazy = 8.f;    // the reference moves once weights pass 2^8
+// Weights are at most 2^kBase when the reference moves, and 2^(kBase + kLazy) before it
+// does, which f16 holds; the less it is let drift, the smaller the weights that f16 still
+// tells apart.  O is in registers, so moving it costs little: 8 and 7, 4 and 11, 2 and 13,
+// 1 and 14 all take 53.0 us for 64 sequences of 4096.
+constexpr float kBase = 13.f;
+constexpr float kLazy = 2.f;
 
 struct StageInfo {
   float k_scale[4];    // per 16 tokens
@@ -567,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? 2 : 1)
           float p[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float r = ref[n][i & 1] == -INFINITY ? 0.f : ref[n][i & 1];
+            const float r = (ref[n][i & 1] == -INFINITY ? 0.f : ref[n][i & 1]) - kBase;
             p[i] = exp2_approx(s[n][i] - r);
             sum[n][i & 1] = fmaf(p[i], v_inv, sum[n][i & 1]);
           }
