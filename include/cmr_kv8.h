@@ -91,8 +91,9 @@ CMR_API cmr_status cmr_kv8_rotate_qk(void* q, const void* k, const void* v,
  *   out[l, t, h, :] = sum_i w_i v_i / sum_i w_i,  w_i = exp(scale * q[l, t, h, :] . k_i)
  * with k_i, v_i of KV head h / (hq / hk).  The sums and the softmax run in fp32;
  * for the product with the codes of the values the weights, times their page's value
- * scale, are rounded: in the kernel for few rows by at most 2^-11 of themselves, or
- * 2^-38 of the row's largest where that is more.  The result is rounded to bf16.  A token with p < 0 sees nothing and gets zeros.
+ * scale, are rounded: in the kernel for few rows (below) by at most 2^-11 of themselves,
+ * or 2^-38 of the row's largest where that is more; in the one for many by 2^-9 + 2^-11,
+ * or 2^-26.  The result is rounded to bf16.  A token with p < 0 sees nothing and gets zeros.
  * Rows behind the last sequence are left as they are.
  * Rows of the pages that a token does not see never reach its result, whatever
  * their codes are (NaN among them).

@@ -11,10 +11,13 @@ from tests.kv8_model import Cache, assert_within, i32
 
 pytestmark = pytest.mark.gpu
 
-# The weights in the products, relative to the row's largest: rounded by `half`
+# The weights of each kernel in its products, relative to the row's largest: rounded by `half`
 # of a weight's own size at most, or by `floor` where that is more.
 #   decode: f16 (half a step 2^-11 of the number, or half of 2^-24), the largest weight at 2^13 or more
+#   prompts: f16, then three terms of e5m2 (half a step 2^-9 together, or half of 2^-16), the
+#            largest at 2^9 or more
 ROWS = dict(half=2.0 ** -11, floor=2.0 ** -25 / 2 ** 13)
+TILES = dict(half=2.0 ** -9 + 2.0 ** -11, floor=(2.0 ** -17 + 2.0 ** -25) / 2 ** 9)
 
 
 def model(q, c, spans, scale, half, floor):
@@ -97,3 +100,12 @@ def test_steps_behind_one_strong_token(cuda_device, margin, varied):
 @pytest.mark.parametrize("margin", MARGINS)
 def test_short_chunks_behind_one_strong_token(cuda_device, margin):
     check(cuda_device, [4, 3], [20000, 900], [0, 899], margin, "attend_rows_kernel", ROWS, D=256)
+
+
+@pytest.mark.parametrize("varied", [False, True])
+@pytest.mark.parametrize("margin", MARGINS)
+def test_prompts_behind_one_strong_token(cuda_device, margin, varied):
+    check(cuda_device, [1500], [0], [0], margin, "attend_tiles_kernel", TILES, hq=2, hk=1,
+          varied=varied)
+    check(cuda_device, [40, 130], [30000, 2000], [0, 1500], margin, "attend_tiles_kernel", TILES,
+          D=256, varied=varied)

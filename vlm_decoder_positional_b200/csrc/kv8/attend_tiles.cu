@@ -12,10 +12,15 @@
 //       2^-19 of it);
 //   p = p1 + p2 + p3, e5m2: e5m2 is the upper byte of f16, so p1 is the upper byte of
 //       p in f16, p2 that of what is left, and p3 that of the rest, rounded: 9
-//       significant bits at least (down to 2^-25 of the row's largest weight).
-// p thus carries half the rounding that bf16 weights would (2^-9), and S and O are fp32
-// accumulators in tensor memory.  The scales enter as in attend_rows.cu: keys' in
-// the exponent's factor, values' in the exponent, and 2^-e in the sum of weights.
+//       significant bits, down to e5m2's smallest number 2^-16.  The row's largest p
+//       lies between 2^9 and 2^15, so a weight of 2^-17 of it or more keeps its 9 bits,
+//       a smaller one is off by 2^-26 of the largest.  Letting the reference drift less
+//       would leave more room below: 2^-28 (base 11, drift 4) takes 2.5 % more time for
+//       4 prompts of 8192, 2^-29 5 %, 2^-30 10 %.
+// A p that keeps its 9 bits carries about half the rounding of a bf16 weight (2^-9 and the
+// 2^-11 of f16 before it, for 2^-8), and S and O are fp32 accumulators in tensor memory.
+// The scales enter as in attend_rows.cu: keys' in the exponent's factor, values' in the
+// exponent, and 2^-e in the sum of weights, which takes p as it is.
 //
 // Bound by the tensor cores: 2 x D steps of QK and 3 x 128 of PV at the 8-bit rate
 // (twice bf16's) are 1.25 x the time of the same product in bf16.  Converting V
