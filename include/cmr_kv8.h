@@ -150,14 +150,16 @@ CMR_API size_t cmr_kv8_attend_workspace_bytes(int32_t num_seqs, int64_t n_tokens
  *   workspace         device memory, 16-byte aligned, of at least
  *                     cmr_kv8_pages_workspace_bytes(table_rows, num_pages, n); as
  *                     for cmr_kv8_attend, overlapping calls need their own
- * A row's entries up to the first negative one are its pages; a page id outside
- * the pool in them sets CMR_DEVICE_CACHE_RANGE and is not followed. */
+ * A row's entries up to the first negative one are its pages, whatever stands behind
+ * it; a page id outside the pool in them sets CMR_DEVICE_CACHE_RANGE and is not
+ * followed (a fork looks at those that it shares or copies from). */
 
 /* Give each named row the pages that it lacks to hold lens[i] tokens (none where
  * it has them).  An entry that needs more than max_pages gets none
  * (CMR_DEVICE_CACHE_RANGE); one that finds too few free pages left, and those behind
  * it that need any, get none (CMR_DEVICE_PAGES_FULL).
- * New pages get page_refs = 1; their codes and scales are left as they are. */
+ * New pages get page_refs = 1; their codes and scales are left as they are.  A page id
+ * outside the pool counts as a page of its row. */
 CMR_API cmr_status cmr_kv8_extend(int32_t* page_table, int32_t table_rows, int32_t max_pages,
                                   int32_t* page_refs, int32_t num_pages, int32_t page_tokens,
                                   const int32_t* slots, const int32_t* lens, int32_t n,
