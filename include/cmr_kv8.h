@@ -192,7 +192,9 @@ CMR_API cmr_status cmr_kv8_free(int32_t* page_table, int32_t table_rows, int32_t
 /* Move pages so that those in use are the pool's first: with c pages in use, the
  * ones at c and above go, in order, to the free ones below c, in every layer,
  * with their scales and counts, and the whole table follows.  page_refs > 0 says
- * that a page is in use.  Page ids held outside the table become stale. */
+ * that a page is in use.  Page ids held outside the table become stale.  Where a row
+ * lists a page of c or above that is not in use, or one outside the pool, its entry is
+ * left as it is (CMR_DEVICE_CACHE_RANGE). */
 CMR_API cmr_status cmr_kv8_compact(void* k_pages, void* v_pages, float* k_scales,
                                    float* v_scales, int32_t num_layers, int32_t hk,
                                    int32_t head_dim, int32_t num_pages, int32_t page_tokens,

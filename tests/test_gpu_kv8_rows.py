@@ -82,3 +82,37 @@ def test_a_forked_row_ends_behind_its_pages(cuda_device):
                  device_status=status)
     assert t.tolist() == [[5, 1, -1, -1], [5, -1, 6, 2], [5, 0, -1, 3]]
     assert refs.tolist() == [1, 1, 0, 0, 0, 3, 0, 0] and int(status.item()) == 0
+
+
+def compact(dev, rows, refs):
+    """(table, counts, status) after the call, as lists."""
+    c = Cache(dev, [], 2, 1, 64, P, spare=len(refs))
+    t, r = i32(rows, dev), i32(refs, dev)
+    status = torch.zeros(1, dtype=torch.int32, device=dev)
+    pkg.kv8_compact(*c.pool(), t, r, device_status=status)
+    return t.tolist(), r.tolist(), int(status.item())
+
+
+def test_compact_flags_what_is_no_page_in_use(cuda_device):
+    # pages 3 and 5 go to 0 and 2; an id outside the pool, and one of a free page, stay
+    refs = [0, 1, 0, 1, 0, 1, 0, 0]
+    rows = [[1, 5, -1, -1], [3, -1, -1, -1]]
+    assert compact(cuda_device, rows, refs) == ([[1, 2, -1, -1], [0, -1, -1, -1]],
+                                                [1, 1, 1, 0, 0, 0, 0, 0], 0)
+    for bad in (8, 2 ** 31 - 1, 7):
+        t, r, st = compact(cuda_device, [[1, bad, 5, -1], [3, -1, -1, -1]], refs)
+        assert (t, st) == ([[1, bad, 2, -1], [0, -1, -1, -1]], RANGE)
+
+
+def test_compact_looks_at_the_table_where_nothing_moves(cuda_device):
+    refs = [1, 1, 1, 0, 0]
+    assert compact(cuda_device, [[0, 1, -1], [2, -1, -1]], refs)[2] == 0
+    for bad in (5, 4):
+        t, r, st = compact(cuda_device, [[0, 1, -1], [2, bad, -1]], refs)
+        assert (t, r, st) == ([[0, 1, -1], [2, bad, -1]], refs, RANGE)
+
+
+def test_compact_leaves_what_stands_behind_a_row(cuda_device):
+    refs = [0, 1, 0, 1, 0, 1, 0, 0]
+    t, r, st = compact(cuda_device, [[1, -1, 9, 7], [-1, 6, -1, 4], [3, 5, -2, 99]], refs)
+    assert (t, st) == ([[1, -1, 9, 7], [-1, 6, -1, 4], [0, 2, -2, 99]], 0)

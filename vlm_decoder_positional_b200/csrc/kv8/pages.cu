@@ -451,7 +451,6 @@ __global__ void __launch_bounds__(kCopyThreads) compact_move_kernel(const PagesA
   const int32_t* from = to + a.pool.num_pages;
   const int moves = __ldcg(a.workspace + kJobs);
   const int live = __ldcg(a.workspace + kLive);
-  if (moves == 0) return;
   const int hk = a.pool.hk;
   const int64_t bytes = static_cast<int64_t>(hk) * a.page_tokens * a.pool.head_dim;
   const int units = a.pool.num_layers * 2;
@@ -480,10 +479,14 @@ __global__ void __launch_bounds__(kCopyThreads) compact_move_kernel(const PagesA
       else
         hi = mid;
     }
-    if (lo < moves && __ldcg(from + lo) == id)
+    if (lo < moves && __ldcg(from + lo) == id) {
       a.table[i] = __ldcg(to + lo);
-    else
-      flag(a, CMR_DEVICE_CACHE_RANGE);
+      continue;
+    }
+    // no page in use: a fault where it is one of its row's pages
+    int64_t k = i - i % a.max_pages;
+    while (k < i && __ldcg(a.table + k) >= 0) ++k;
+    if (k == i) flag(a, CMR_DEVICE_CACHE_RANGE);
   }
 }
 
