@@ -69,7 +69,8 @@ extern "C" {
  *                     are, and the page gets the new rows' scale),
  *                     CMR_DEVICE_BAD_CU_SEQLENS (the sequences involved
  *                     are skipped)
- * hq may be 0 (q NULL); hk >= 1.  q, k, v, k_pages and v_pages 16-byte aligned.
+ * hq may be 0 (q NULL); hk >= 1.  q, k, v, k_pages and v_pages 16-byte aligned; q must
+ * not overlap k or v, nor any of them the pages.
  * Errors: CMR_EINVAL for any violation above, CMR_EUNSUPPORTED for another
  * head_dim or page_tokens, hk * head_dim over 2^23, hk * num_layers over 65535, or
  * num_layers * num_pages * hk or (hq + hk) * num_layers over INT32_MAX. */

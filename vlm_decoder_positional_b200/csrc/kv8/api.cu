@@ -322,6 +322,17 @@ cmr_status cmr_kv8_rotate_qk(void* q, const void* k, const void* v, const int32_
   if ((s = check(start, "start")) != CMR_OK) return s;
   if ((s = check(amount, "amount")) != CMR_OK) return s;
   if ((s = check(slot, "slot", 4, true)) != CMR_OK) return s;
+  const int64_t per_head = static_cast<int64_t>(num_layers) * n_tokens * head_dim * 2;
+  const int64_t pool = static_cast<int64_t>(num_layers) * num_pages * hk * page_tokens * head_dim;
+  const struct {
+    const void* p;
+    int64_t bytes;
+  } made[] = {{q, hq * per_head}, {k_pages, pool}, {v_pages, pool}},
+    given[] = {{k, hk * per_head}, {v, hk * per_head}, {k_pages, pool}, {v_pages, pool}};
+  for (int i = hq > 0 ? 0 : 1; i < 3; ++i)  // of the pages: only k and v
+    for (int j = 0; j < (i == 0 ? 4 : 2); ++j)
+      if (overlap(made[i].p, made[i].bytes, given[j].p, given[j].bytes))
+        return fail(CMR_EINVAL, "q, k or v overlaps what the call writes");
   const Named list[] = {{hq ? q : nullptr, "q"}, {k, "k"}, {v, "v"}, {cu_seqlens, "cu_seqlens"},
                         {pos_offset, "pos_offset"}, {start, "start"}, {amount, "amount"},
                         {k_pages, "k_pages"}, {v_pages, "v_pages"}, {k_scales, "k_scales"},
