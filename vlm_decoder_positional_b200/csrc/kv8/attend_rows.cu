@@ -26,7 +26,7 @@
 // four warps take 16 tokens of a tile each: S^T = K Q^T with the tokens as the
 // rows of mma.m16n8k16, whose fragments are then consecutive bytes of a key, and
 // O^T += V^T P^T, whose fragments are bytes of two tokens woven together by prmt.
-// The tensor work is a few percent of the time, so tcgen05 would gain nothing.
+// The tensor pipe is busy in 16 % of the cycles, so tcgen05 would gain nothing.
 // Measured, 8 query and 2 KV heads of 256, pages of 64: 64 sequences of 4096 53 us
 // (5.1 TB/s, 79% of a copy's rate), one of 262144 55 us, 128 of 1 to 8192 29 us where
 // the bytes alone take 15: what is left is the start of the two kernels and the last
@@ -280,9 +280,11 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? 2 : 1)
     };
     int stage = 0, phase = 0, issued = 0;
     bool dead = false;
-    // The cache is read once and marked so in L2, where tables, scales and partial results
-    // stay: 53 us instead of 57 for 64 sequences of 4096, 54.5 instead of 59 for one of
-    // 262144.
+    // A sequence's pages are read once and marked so in L2, where tables, scales and partial
+    // results stay: 53 us instead of 57 for 64 sequences of 4096, 54.5 instead of 59 for one
+    // of 262144.  Pages that branches share are read by each of them: 64 branches of 4000
+    // tokens or of 500 take the same either way (51 and 22.5 us), 8 of 20000 41 us marked
+    // and 39 not, 16 of 100000 262 and 231; the call does not know which pages are shared.
     const uint64_t policy = tma::l2_evict_first_policy();
     Look now = look(run_lo);
     for (uint32_t w = run_lo; w < run_hi && !dead; w += 8) {
@@ -1008,7 +1010,10 @@ cudaError_t launch(const RowsArgs& ra, const CUtensorMap& k, const CUtensorMap& 
   if (e != cudaSuccess || ra.ctas == 1) return e;
   // With one item to four runs or more, an item is cut into a few pieces: a CTA
   // joins them all.  With fewer items there are many pieces, and the CTAs share
-  // an item's rows and dims.
+  // an item's rows and dims.  By the first way and by the second (one token each, two KV
+  // heads, replayed from a graph with cold caches): one sequence of 700 18.4 and 14.3 us,
+  // one of 20000 55 and 20, 8 of 4000 29 and 26, 16 of 4000 31 and 31, 36 43 and 47, 64 61
+  // and 70, 128 104 and 121.
   if (ra.items * lh * 4 >= ra.ctas)
     return pdl::launch(attend_join_runs_kernel<D, NQ>, dim3(ra.ctas), dim3(kJoinThreads), 0, stream,
                        true, ra);
@@ -1091,9 +1096,17 @@ namespace {
 // one sequence's.  Up to 8, such a call is shared out: the sequences of more than
 // kFewRows rows go to the one kernel, the others to the other.  63 sequences of one
 // token behind 2000 and one of 60 behind 100000 take 120 us so and 428 by rows alone, one
-// of 128 179 and 876; that costs 8 us where there was nothing to share out (64 of one
-// token behind 4000, called with cu_seqlens: 63 us instead of 55).
-constexpr int kSmallCall = 64;  // rows in all, for which a second kernel does not pay
+// of 128 179 and 876.  Where there was nothing to share out that costs a second launch,
+// with a CTA for each row tile that there might be: 8 us for 64 sequences of one token
+// behind 4000 (55 to 63), 12 for 64 behind 500 (27 to 39), 27 for 256 (45 to 72), 82 for 1024
+// (184 to 266).
+// Above 8 rows on average the tcgen05 kernel has the single tokens too, each in a tile of
+// 128 rows: 63 of them behind 4000 and a prompt of 2048 take 121 us, and 154 by both.
+// A call of up to kSmallCall rows is not shared out.  64 rows, of 13 tokens and three
+// single ones: behind 200 tokens 16 us by rows and 26 by tiles, behind 2000 25 and 27, behind
+// 20000 57 and 45; of 5 tokens and seven single ones, by rows and by both: 16 and 27, 25
+// and 32, 55 and 63.
+constexpr int kSmallCall = 64;
 constexpr int kFewRows = 32;
 
 struct Kernels {

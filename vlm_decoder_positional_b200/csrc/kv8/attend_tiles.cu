@@ -911,8 +911,11 @@ __global__ void __launch_bounds__(kJoinThreads) attend_tiles_join_kernel(const T
                                               pack_bf16x2(acc.z * inv, acc.w * inv));
 }
 
-// The multiprocessors that items are split among: above kPlanned sequences the plan would
-// cost more than it saves, and with more heads than half of them no item has two pieces.
+// The multiprocessors that items are split among.  Each CTA works the plan out for itself,
+// 32 sequences at a time: with it and without, 64 chunks of 6 tokens behind 500 take 35
+// and 25 us, 256 108 and 82, 512 238 and 143, 1024 637 and 277; with one of 100 behind 20000
+// among them 72 and 297, 131 and 352, 258 and 423, 661 and 557.  So up to kPlanned sequences;
+// and with more heads than half of the multiprocessors no item has two pieces.
 int split_among(int32_t num_seqs, int64_t heads) {
   return num_seqs <= kPlanned && 2 * heads <= sm_count() ? sm_count() : 0;
 }
@@ -930,7 +933,9 @@ cudaError_t launch(const TilesArgs& ta, const CUtensorMap& k, const CUtensorMap&
                   k, v);
   if (e != cudaSuccess || ta.sms == 0) return e;
   // With few items there are many pieces of each: the threads of a CTA share those of one
-  // row.
+  // row.  So and without (two KV heads, replayed from a graph with cold caches): one chunk of
+  // 40 tokens behind 20000, 4 slots, 35 and 47 us; two of 100 behind 6000, 16 slots, 43 and
+  // 39; four, 32 slots, 57 and 51; eight of 60 behind 3000, 46 slots, 49 and 41.
   constexpr int kPer = kJoinThreads / (D / 4);
   const unsigned room = static_cast<unsigned>(ta.room * lh);
   if (ta.items * lh <= 16)
